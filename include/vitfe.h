@@ -251,6 +251,169 @@ vitfe_status vitfe_items_from_grid(const int32_t* grid_thw, const uint8_t* is_st
                                    int patch, int tpatch, vitfe_item* items_out,
                                    int64_t* total_rows, int64_t* pixel_bytes);
 
+/* ---------------------------------------------------------------------------
+ * Encoder-block operators: what runs behind the patch embeddings.  None needs a
+ * handle; all are capturable, allocate nothing and follow the conventions above
+ * (caller-owned device memory, host argument errors launch nothing, device-side
+ * errors in the optional status pair).  They launch as ordinary stream work.
+ * Rows have a stride in elements and are contiguous inside, so a tensor may be
+ * a view into a wider one (Q, K and V inside one projection's rows).
+ * ------------------------------------------------------------------------- */
+
+typedef enum { VITFE_BF16 = 0, VITFE_F16 = 1, VITFE_F32 = 2 } vitfe_dtype;
+
+#define VITFE_NORM_MAX_WIDTH 16384 /* widest row of the layer norm                  */
+#define VITFE_MAX_SPANS 1024       /* spans per vitfe_mrope_positions call          */
+#define VITFE_MAX_AXES 4           /* position axes of vitfe_mrope_apply            */
+#define VITFE_ATTN_MAX_HEAD_DIM 128
+#define VITFE_ATTN_MAX_GROUP 64    /* query heads to one key head                   */
+
+/* Layer norm: y = (x - mean) * rstd * weight + bias over each row of `width`
+ * elements, mean = sum(x)/width, rstd = 1/sqrt(sum((x - mean)^2)/width + eps).
+ * x, out: [rows] of `dtype` (strides in elements, >= width); out may be x.
+ * weight, bias: [width] of param_dtype, or NULL (1 and 0).  mean, rstd: fp32
+ * [rows] or NULL; the backward pass takes them.  Statistics in fp32 (two passes
+ * over the row in registers), one rounding at the store.  Pointers aligned to
+ * their element; 16-byte aligned rows (base and stride) take 16-byte accesses.
+ * 1 <= width <= VITFE_NORM_MAX_WIDTH; eps >= 0 and finite. */
+vitfe_status vitfe_layer_norm(const void* x, int64_t x_row_stride, vitfe_dtype dtype, int64_t rows,
+                              int32_t width, const void* weight, const void* bias,
+                              vitfe_dtype param_dtype, float eps, void* out,
+                              int64_t out_row_stride, float* mean, float* rstd,
+                              cudaStream_t stream);
+
+/* Its gradients.  With xh = (x - mean) * rstd and g = dout * weight:
+ *   dx = rstd * (g - sum(g)/width - xh * sum(g * xh)/width)     per row
+ *   dweight = sum over rows of dout * xh,  dbias = sum over rows of dout
+ * mean, rstd: fp32 [rows] of the forward pass.  dx: [rows] of `dtype`; may be
+ * dout or x.  dweight, dbias: fp32 [width], either may be NULL; written, not
+ * accumulated (0 for rows == 0).  The sums over rows are fp32 in a fixed order:
+ * equal calls give equal bits.
+ * workspace (16-byte aligned): vitfe_layer_norm_workspace(rows, width) bytes; may
+ * be NULL when dweight and dbias are. */
+vitfe_status vitfe_layer_norm_backward(const void* dout, int64_t dout_row_stride, const void* x,
+                                       int64_t x_row_stride, vitfe_dtype dtype, int64_t rows,
+                                       int32_t width, const void* weight, vitfe_dtype param_dtype,
+                                       const float* mean, const float* rstd, void* dx,
+                                       int64_t dx_row_stride, float* dweight, float* dbias,
+                                       void* workspace, int64_t workspace_bytes,
+                                       cudaStream_t stream);
+int64_t vitfe_layer_norm_workspace(int64_t rows, int32_t width);
+
+/* One span of a packed prompt (device-resident, 16 bytes): `text` text tokens,
+ * then, for item >= 0, the merged patches of that item (t * h/merge * w/merge
+ * tokens, time-major, then rows, then columns: the merge order of its groups).
+ * first != 0 starts a sequence: positions begin at 0 again. */
+typedef struct {
+  int32_t first;
+  int32_t text;
+  int32_t item;   /* -1: no item */
+  int32_t step;   /* time positions from one temporal group to the next, 0 .. 65536 */
+} vitfe_span;
+
+/* Positions of a packed prompt on three axes (time, height, width), int32
+ * [3][rows].  A text token takes the sequence's next position on all three; an
+ * item that starts at position p gives its token (tg, y, x) the positions
+ * (p + tg * step, p + y, p + x), and what follows it starts at
+ * p + max((t - 1) * step + 1, h/merge, w/merge).  Rows past the last token: -1.
+ * spans (device vitfe_span[max_spans]), n_spans (device int32), max_spans <=
+ * VITFE_MAX_SPANS; items, n_items, max_items: as in the calls above (only t, h
+ * and w are read; may be NULL with max_items 0).  Device errors in `status`
+ * {code, span}: VITFE_EDEVICE_DESC for an inconsistent span or grid (it counts
+ * as empty), VITFE_EDEVICE_RANGE for more tokens than rows, or positions past
+ * 2^31 - 1 (clamped). */
+vitfe_status vitfe_mrope_positions(const vitfe_span* spans, const int32_t* n_spans,
+                                   int32_t max_spans, const vitfe_item* items,
+                                   const int32_t* n_items, int32_t max_items, int32_t merge,
+                                   int64_t rows, int32_t* pos, int32_t* status,
+                                   cudaStream_t stream);
+
+/* Rotary positions with several axes, applied to Q and K.  Pair i (of
+ * rotary_dim / 2) of a head turns by the angle pos[axis_of_pair[i]][row] * w_i,
+ * w_i = theta^(-2i/rotary_dim), in the rotate-half form of vitfe_rope_apply over
+ * the head's first rotary_dim elements; the rest is copied.  inverse != 0 turns
+ * the other way: the gradient of the call, and its undoing.
+ * pos: device int32 [axes][rows]; axis_of_pair: HOST uint8 [rotary_dim / 2],
+ * values below axes <= VITFE_MAX_AXES.  Angles are exact to 2^-32 turns at any
+ * position (integer phases).  q: [rows][heads_q][head_dim] with a row stride,
+ * q_out likewise, and may be q; k, k_out likewise; heads_q or heads_k may be 0
+ * (those pointers are then unused).  Bases 8-byte aligned (fp32: 16), strides
+ * multiples of 4 elements.  head_dim % 8 == 0, rotary_dim % 8 == 0,
+ * 8 <= rotary_dim <= head_dim <= VITFE_ROPE_MAX_HEAD_DIM. */
+vitfe_status vitfe_mrope_apply(const int32_t* pos, int32_t axes, const uint8_t* axis_of_pair,
+                               int32_t rotary_dim, float theta, int32_t inverse, int64_t rows,
+                               int32_t head_dim, vitfe_dtype dtype, const void* q, int32_t heads_q,
+                               int64_t q_row_stride, void* q_out, int64_t q_out_row_stride,
+                               const void* k, int32_t heads_k, int64_t k_row_stride, void* k_out,
+                               int64_t k_out_row_stride, cudaStream_t stream);
+
+/* Attention over packed sequences.  Sequence s holds the query rows
+ * [cu_q[s], cu_q[s+1]) and the key rows [cu_k[s], cu_k[s+1]); either may be empty.
+ * Query head h reads key head h / (heads_q / heads_kv).
+ *   out = softmax(scale * q k^T) v over the keys that the row sees.
+ * causal: the last query row of a sequence sees all its keys, the one before it
+ * all but the last, and so on (a new token sees its whole cache).  A row that
+ * sees no key (fewer keys than query rows, or none) gives 0 and lse -inf, and
+ * so do rows of no sequence.  Values in rows of other sequences and in the
+ * padding are never mixed in, whatever they hold.  Inside a sequence a key that
+ * the causal mask hides counts with weight 0, so a NaN or infinity in its V
+ * can reach earlier rows, as 0 * NaN does in the formula. */
+typedef struct {
+  int64_t rows_q, rows_k;    /* rows of q, out, lse and of k, v (padding included)   */
+  int32_t max_seqs;          /* cu_q and cu_k hold max_seqs + 1 entries              */
+  int32_t heads_q, heads_kv; /* heads_q a multiple, at most VITFE_ATTN_MAX_GROUP times */
+  int32_t head_dim;          /* a multiple of 8, 8 .. VITFE_ATTN_MAX_HEAD_DIM        */
+  int32_t causal;
+  vitfe_dtype dtype;         /* VITFE_BF16 or VITFE_F16: q, k, v, out and gradients  */
+} vitfe_attention_shape;
+
+/* The plan of a batch: which tiles of which sequences there are, largest first, and
+ * how long key ranges are cut for few query rows.  Made on the device from the
+ * boundaries (so a captured graph replays with new ones), once for all layers of a
+ * batch; read-only afterwards, so calls on several streams may share it.
+ * cu_q, cu_k (device int32 [max_seqs + 1]; the layout of vitfe_cu_seqlens, whose
+ * entries past the last sequence repeat its end).  Boundaries that decrease, do not
+ * start at 0 or pass rows_q / rows_k: status {VITFE_EDEVICE_DESC, sequence}, and the
+ * plan holds no sequence (all rows are padding).  The plan depends on every field
+ * of the shape but dtype.  plan: 16-byte aligned,
+ * vitfe_attention_plan_bytes(shape) bytes (0 for an invalid shape). */
+int64_t vitfe_attention_plan_bytes(const vitfe_attention_shape* shape);
+vitfe_status vitfe_attention_plan(const vitfe_attention_shape* shape, const int32_t* cu_q,
+                                  const int32_t* cu_k, void* plan, int32_t* status,
+                                  cudaStream_t stream);
+
+/* q: [rows_q][heads_q][head_dim], k, v: [rows_k][heads_kv][head_dim], out as q; row
+ * strides in elements, multiples of 8; bases 16-byte aligned.  scale > 0, finite.
+ * lse: fp32 [rows_q][heads_q] (natural log of the sum of exponentials of the scaled
+ * scores) or NULL.  Scores, maxima, sums and the output's accumulator are fp32; the
+ * probabilities are rounded to dtype for their product with V.
+ * workspace: 16-byte aligned, vitfe_attention_workspace(shape) bytes (may be 0); one
+ * call at a time may use it.  status (device int32[2]) or NULL: {0, -1}, or
+ * {VITFE_EDEVICE_TIMEOUT, -1} when a bounded wait ran out (outputs invalid). */
+int64_t vitfe_attention_workspace(const vitfe_attention_shape* shape);
+vitfe_status vitfe_attention(const vitfe_attention_shape* shape, const void* plan, const void* q,
+                             int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                             const void* v, int64_t v_row_stride, float scale, void* out,
+                             int64_t out_row_stride, float* lse, void* workspace, int32_t* status,
+                             cudaStream_t stream);
+
+/* Its gradients: with p = exp(scale * q k^T - lse), dp = dout v^T and
+ * delta = sum(dout * out) per row and head,
+ *   dv = p^T dout,  ds = p * (dp - delta),  dq = scale * ds k,  dk = scale * ds^T q,
+ * dk and dv summed over the query heads that share a key head, in a fixed order:
+ * equal calls give equal bits.  out, lse: the forward pass's.  Rows of no sequence
+ * get 0.  p and ds are rounded to dtype for their products; sums are fp32.
+ * workspace: vitfe_attention_backward_workspace(shape) bytes, as above. */
+int64_t vitfe_attention_backward_workspace(const vitfe_attention_shape* shape);
+vitfe_status vitfe_attention_backward(const vitfe_attention_shape* shape, const void* plan,
+                                      const void* dout, int64_t dout_row_stride, const void* q,
+                                      int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                      const void* v, int64_t v_row_stride, const void* out,
+                                      int64_t out_row_stride, const float* lse, float scale,
+                                      void* dq, int64_t dq_row_stride, void* dk,
+                                      int64_t dk_row_stride, void* dv, int64_t dv_row_stride,
+                                      void* workspace, int32_t* status, cudaStream_t stream);
+
 /* Feature width K = 3*tpatch*patch*patch of a handle (0 for NULL). */
 int vitfe_feature_dim(vitfe_t h);
 

@@ -18,6 +18,12 @@ LIB_PATH = os.path.join(PKG, "libvitfe.so")
 
 VITFE_MAX_ITEMS = 256
 VITFE_ROPE_MAX_SIDE = 4096
+VITFE_NORM_MAX_WIDTH = 16384
+VITFE_MAX_SPANS = 1024
+VITFE_MAX_AXES = 4
+VITFE_ATTN_MAX_HEAD_DIM = 128
+VITFE_ATTN_MAX_GROUP = 64
+VITFE_BF16, VITFE_F16, VITFE_F32 = 0, 1, 2
 
 STATUS_NAMES = {0: "VITFE_OK", 1: "VITFE_EINVAL", 2: "VITFE_ENOMEM", 3: "VITFE_ECUDA",
                 4: "VITFE_EDEVICE_DESC", 5: "VITFE_EDEVICE_RANGE", 6: "VITFE_EDEVICE_TIMEOUT",
@@ -28,6 +34,10 @@ EXPORTS = ["vitfe_create", "vitfe_destroy", "vitfe_embed", "vitfe_embed_rope", "
            "vitfe_embed_folded", "vitfe_rope", "vitfe_normalize_patchify",
            "vitfe_pos_ids", "vitfe_cu_seqlens", "vitfe_rope_apply", "vitfe_rope_noalloc",
            "vitfe_items_from_grid",
+           "vitfe_layer_norm", "vitfe_layer_norm_backward", "vitfe_layer_norm_workspace",
+           "vitfe_mrope_positions", "vitfe_mrope_apply",
+           "vitfe_attention_plan_bytes", "vitfe_attention_plan", "vitfe_attention_workspace", "vitfe_attention",
+           "vitfe_attention_backward_workspace", "vitfe_attention_backward",
            "vitfe_feature_dim", "vitfe_status_str"]
 
 ITEM_DTYPE = np.dtype([("pixel_offset", "<i8"), ("t", "<i4"), ("h", "<i4"), ("w", "<i4"),
@@ -38,6 +48,13 @@ assert ITEM_DTYPE.itemsize == 24
 class VitfeItem(ctypes.Structure):
     _fields_ = [("pixel_offset", ctypes.c_int64), ("t", ctypes.c_int32), ("h", ctypes.c_int32),
                 ("w", ctypes.c_int32), ("frames", ctypes.c_int32)]
+
+
+class AttentionShape(ctypes.Structure):
+    """vitfe_attention_shape."""
+    _fields_ = [("rows_q", ctypes.c_int64), ("rows_k", ctypes.c_int64), ("max_seqs", ctypes.c_int32),
+                ("heads_q", ctypes.c_int32), ("heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class VitfeError(RuntimeError):
@@ -86,6 +103,29 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.vitfe_items_from_grid.argtypes = [P, P, I32, ctypes.c_int, ctypes.c_int, P,
                                           ctypes.POINTER(I64), ctypes.POINTER(I64)]
     lib.vitfe_items_from_grid.restype = ctypes.c_int
+    CI = ctypes.c_int
+    lib.vitfe_layer_norm.argtypes = [P, I64, CI, I64, I32, P, P, CI, F32, P, I64, P, P, P]
+    lib.vitfe_layer_norm.restype = CI
+    lib.vitfe_layer_norm_backward.argtypes = [P, I64, P, I64, CI, I64, I32, P, CI, P, P, P, I64, P, P, P, I64, P]
+    lib.vitfe_layer_norm_backward.restype = CI
+    lib.vitfe_layer_norm_workspace.argtypes = [I64, I32]
+    lib.vitfe_layer_norm_workspace.restype = I64
+    lib.vitfe_mrope_positions.argtypes = [P, P, I32, P, P, I32, I32, I64, P, P, P]
+    lib.vitfe_mrope_positions.restype = CI
+    lib.vitfe_mrope_apply.argtypes = [P, I32, P, I32, F32, I32, I64, I32, CI, P, I32, I64, P, I64, P, I32, I64, P,
+                                      I64, P]
+    lib.vitfe_mrope_apply.restype = CI
+    SH = ctypes.POINTER(AttentionShape)
+    lib.vitfe_attention_plan.argtypes = [SH, P, P, P, P, P]
+    lib.vitfe_attention_plan.restype = CI
+    for fn in (lib.vitfe_attention_plan_bytes, lib.vitfe_attention_workspace, lib.vitfe_attention_backward_workspace):
+        fn.argtypes = [SH]
+        fn.restype = I64
+    lib.vitfe_attention.argtypes = [SH, P, P, I64, P, I64, P, I64, F32, P, I64, P, P, P, P]
+    lib.vitfe_attention.restype = CI
+    lib.vitfe_attention_backward.argtypes = [SH, P, P, I64, P, I64, P, I64, P, I64, P, I64, P, F32, P, I64, P, I64,
+                                             P, I64, P, P, P]
+    lib.vitfe_attention_backward.restype = CI
     lib.vitfe_feature_dim.argtypes = [P]
     lib.vitfe_feature_dim.restype = ctypes.c_int
     lib.vitfe_status_str.argtypes = [ctypes.c_int]
@@ -229,6 +269,85 @@ def vitfe_items_from_grid(grid_thw: np.ndarray, is_still: Optional[np.ndarray], 
                                      int(patch), int(tpatch), items.ctypes.data if n else None,
                                      ctypes.byref(rows), ctypes.byref(nbytes)))
     return items, int(rows.value), int(nbytes.value)
+
+
+def vitfe_layer_norm(x, x_row_stride, dtype, rows, width, weight, bias, param_dtype, eps, out, out_row_stride,
+                     mean=None, rstd=None, stream=None) -> None:
+    _check("vitfe_layer_norm", load().vitfe_layer_norm(_ptr(x), int(x_row_stride), int(dtype), int(rows), int(width),
+                                                       _ptr(weight), _ptr(bias), int(param_dtype), float(eps),
+                                                       _ptr(out), int(out_row_stride), _ptr(mean), _ptr(rstd),
+                                                       _stream(stream)))
+
+
+def vitfe_layer_norm_workspace(rows: int, width: int) -> int:
+    return int(load().vitfe_layer_norm_workspace(int(rows), int(width)))
+
+
+def vitfe_layer_norm_backward(dout, dout_row_stride, x, x_row_stride, dtype, rows, width, weight, param_dtype, mean,
+                              rstd, dx, dx_row_stride, dweight, dbias, workspace, workspace_bytes,
+                              stream=None) -> None:
+    _check("vitfe_layer_norm_backward",
+           load().vitfe_layer_norm_backward(_ptr(dout), int(dout_row_stride), _ptr(x), int(x_row_stride), int(dtype),
+                                            int(rows), int(width), _ptr(weight), int(param_dtype), _ptr(mean),
+                                            _ptr(rstd), _ptr(dx), int(dx_row_stride), _ptr(dweight), _ptr(dbias),
+                                            _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def vitfe_mrope_positions(spans, n_spans, max_spans, items, n_items, max_items, merge, rows, pos, status=None,
+                          stream=None) -> None:
+    _check("vitfe_mrope_positions",
+           load().vitfe_mrope_positions(_ptr(spans), _ptr(n_spans), int(max_spans), _ptr(items), _ptr(n_items),
+                                        int(max_items), int(merge), int(rows), _ptr(pos), _ptr(status),
+                                        _stream(stream)))
+
+
+def vitfe_mrope_apply(pos, axes, axis_of_pair, rotary_dim, theta, inverse, rows, head_dim, dtype, q, heads_q,
+                      q_row_stride, q_out, q_out_row_stride, k, heads_k, k_row_stride, k_out, k_out_row_stride,
+                      stream=None) -> None:
+    """axis_of_pair: bytes, one per pair (at least rotary_dim / 2), or None."""
+    if axis_of_pair is not None and len(axis_of_pair) < int(rotary_dim) // 2:
+        raise VitfeError("vitfe_mrope_apply", 1)
+    _check("vitfe_mrope_apply",
+           load().vitfe_mrope_apply(_ptr(pos), int(axes), axis_of_pair, int(rotary_dim), float(theta), int(inverse),
+                                    int(rows), int(head_dim), int(dtype), _ptr(q), int(heads_q), int(q_row_stride),
+                                    _ptr(q_out), int(q_out_row_stride), _ptr(k), int(heads_k), int(k_row_stride),
+                                    _ptr(k_out), int(k_out_row_stride), _stream(stream)))
+
+
+def vitfe_attention_plan_bytes(shape: AttentionShape) -> int:
+    return int(load().vitfe_attention_plan_bytes(shape))
+
+
+def vitfe_attention_plan(shape: AttentionShape, cu_q, cu_k, plan, status=None, stream=None) -> None:
+    _check("vitfe_attention_plan", load().vitfe_attention_plan(shape, _ptr(cu_q), _ptr(cu_k), _ptr(plan),
+                                                               _ptr(status), _stream(stream)))
+
+
+def vitfe_attention_workspace(shape: AttentionShape) -> int:
+    return int(load().vitfe_attention_workspace(shape))
+
+
+def vitfe_attention(shape: AttentionShape, plan, q, q_row_stride, k, k_row_stride, v, v_row_stride, scale, out,
+                    out_row_stride, lse=None, workspace=None, status=None, stream=None) -> None:
+    _check("vitfe_attention",
+           load().vitfe_attention(shape, _ptr(plan), _ptr(q), int(q_row_stride), _ptr(k), int(k_row_stride), _ptr(v),
+                                  int(v_row_stride), float(scale), _ptr(out), int(out_row_stride), _ptr(lse),
+                                  _ptr(workspace), _ptr(status), _stream(stream)))
+
+
+def vitfe_attention_backward_workspace(shape: AttentionShape) -> int:
+    return int(load().vitfe_attention_backward_workspace(shape))
+
+
+def vitfe_attention_backward(shape: AttentionShape, plan, dout, dout_row_stride, q, q_row_stride, k, k_row_stride, v,
+                             v_row_stride, out, out_row_stride, lse, scale, dq, dq_row_stride, dk, dk_row_stride, dv,
+                             dv_row_stride, workspace=None, status=None, stream=None) -> None:
+    _check("vitfe_attention_backward",
+           load().vitfe_attention_backward(shape, _ptr(plan), _ptr(dout), int(dout_row_stride), _ptr(q),
+                                           int(q_row_stride), _ptr(k), int(k_row_stride), _ptr(v), int(v_row_stride),
+                                           _ptr(out), int(out_row_stride), _ptr(lse), float(scale), _ptr(dq),
+                                           int(dq_row_stride), _ptr(dk), int(dk_row_stride), _ptr(dv),
+                                           int(dv_row_stride), _ptr(workspace), _ptr(status), _stream(stream)))
 
 
 def vitfe_feature_dim(h) -> int:

@@ -1,0 +1,128 @@
+// Definitions shared by the encoder-block operators (layer norm, multi-axis rotary, attention).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "vitfe_internal.cuh"
+
+namespace vitfe {
+
+// ---------------------------------------------------------------------------
+// element types
+// ---------------------------------------------------------------------------
+__host__ __device__ constexpr int dtype_bytes(vitfe_dtype d) { return d == VITFE_F32 ? 4 : 2; }
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+
+// Two floats rounded to nearest even and packed, `lo` in the lower half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// V consecutive elements as one access of V * sizeof(T) bytes (at most 16).
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
+};
+
+// V parameters of any type as floats (the pointer aligned to 16 bytes when V > 1).
+template <int V>
+__device__ __forceinline__ void load_params(const void* p, vitfe_dtype d, int c, float (&out)[V]) {
+  if (d == VITFE_F32) {
+    constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+      const Vec<float, W> x = *reinterpret_cast<const Vec<float, W>*>(static_cast<const float*>(p) + c + i);
+#pragma unroll
+      for (int e = 0; e < W; ++e) out[i + e] = x.v[e];
+    }
+  } else if (d == VITFE_BF16) {
+    const Vec<__nv_bfloat16, V> x =
+        *reinterpret_cast<const Vec<__nv_bfloat16, V>*>(static_cast<const __nv_bfloat16*>(p) + c);
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = to_f32(x.v[e]);
+  } else {
+    const Vec<__half, V> x = *reinterpret_cast<const Vec<__half, V>*>(static_cast<const __half*>(p) + c);
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = to_f32(x.v[e]);
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const void* x;
+  int64_t x_stride;
+  vitfe_dtype dtype;
+  int64_t rows;
+  int width;
+  const void* weight;
+  const void* bias;
+  vitfe_dtype param_dtype;
+  float eps;
+  void* out;            // y, or dx
+  int64_t out_stride;
+  float* mean;          // written by the forward pass, read by the backward pass
+  float* rstd;
+  const void* dout;     // backward only, as the next ones
+  int64_t dout_stride;
+  float* dweight;
+  float* dbias;
+  float* partial;       // [CTA][2][width]
+};
+cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_layer_norm_backward(const NormArgs& a, cudaStream_t s);
+int64_t layer_norm_workspace(int64_t rows, int width);
+
+struct MropeArgs {
+  const int32_t* pos;
+  int axes;
+  const uint8_t* axis_of_pair;   // host
+  int rotary_dim;
+  float theta;
+  bool inverse;
+  int64_t rows;
+  int head_dim;
+  vitfe_dtype dtype;
+  const void* x[2];              // Q, K
+  void* y[2];
+  int heads[2];
+  int64_t x_stride[2], y_stride[2];
+};
+cudaError_t launch_mrope_apply(const MropeArgs& a, cudaStream_t s);
+cudaError_t launch_mrope_positions(const vitfe_span* spans, const int32_t* n_spans, int max_spans,
+                                   const vitfe_item* items, const int32_t* n_items, int max_items, int merge,
+                                   int64_t rows, int32_t* pos, int32_t* status, cudaStream_t s);
+
+}  // namespace vitfe

@@ -12,13 +12,7 @@ struct vitfe_ctx {
   vitfe::Ctx c;
 };
 
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_tiled() {
+vitfe::EncodeTiledFn vitfe::encode_tiled_fn() {
   static EncodeTiledFn fn = nullptr;
   if (fn == nullptr) {
     void* p = nullptr;
@@ -30,6 +24,8 @@ EncodeTiledFn get_encode_tiled() {
   }
   return fn;
 }
+
+namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -232,7 +228,7 @@ vitfe_status vitfe_create(vitfe_t* out, const float mean[3], const float std_[3]
       free_ctx(h);
       return VITFE_ECUDA;
     }
-    EncodeTiledFn enc = get_encode_tiled();
+    vitfe::EncodeTiledFn enc = vitfe::encode_tiled_fn();
     if (enc == nullptr) {
       free_ctx(h);
       return VITFE_ECUDA;

@@ -1,0 +1,281 @@
+// Rotary positions with several axes: the positions of a packed prompt, and their rotation of
+// Q and K.
+#include <cmath>
+
+#include "vitfe_block.cuh"
+
+namespace vitfe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxSpans = VITFE_MAX_SPANS;
+constexpr int kMaxPairs = VITFE_ROPE_MAX_HEAD_DIM / 2;
+
+// ---------------------------------------------------------------------------
+// positions
+// ---------------------------------------------------------------------------
+struct SpanScan {          // an inclusive scan's element: positions restart at a `first` span
+  long long tokens;
+  long long reach;         // positions since the last restart
+  int restart;
+};
+
+__device__ __forceinline__ SpanScan scan_join(const SpanScan& a, const SpanScan& b) {
+  return SpanScan{a.tokens + b.tokens, b.restart ? b.reach : a.reach + b.reach, a.restart | b.restart};
+}
+
+// Every block scans the span table (it is small) and then places its own tokens.
+__global__ void __launch_bounds__(kThreads) mrope_positions_kernel(
+    const vitfe_span* __restrict__ spans, const int32_t* __restrict__ n_spans, int max_spans,
+    const vitfe_item* __restrict__ items, const int32_t* __restrict__ n_items, int max_items, int merge, int rows,
+    int32_t* __restrict__ pos, int32_t* __restrict__ status) {
+  __shared__ int start[kMaxSpans + 1];           // first token, clamped to rows
+  __shared__ int base[kMaxSpans];                // position of the span's first token
+  __shared__ int text[kMaxSpans], step[kMaxSpans], height[kMaxSpans], wide[kMaxSpans];
+  __shared__ SpanScan warp_total[kThreads / 32];
+  __shared__ unsigned first_bad;                 // (span << 4) | code of the first bad span
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int n = *n_spans;
+  int code = kOk;
+  if (n < 0 || n > max_spans) {
+    code = kDesc;
+    n = 0;
+  }
+  int ni = max_items > 0 ? *n_items : 0;
+  if (ni < 0 || ni > max_items) {
+    code = kDesc;
+    n = 0;
+  }
+  if (tid == 0) first_bad = 0xffffffffu;
+  __syncthreads();
+  SpanScan carry{0, 0, 0};
+  for (int b = 0; b < n; b += kThreads) {
+    const int i = b + tid;
+    SpanScan e{0, 0, 0};
+    if (i < n) {
+      const vitfe_span sp = spans[i];
+      bool bad = sp.text < 0 || sp.item < -1 || sp.item >= ni || sp.step < 0 || sp.step > 65536;
+      long long t = 0, h = 0, w = 0;
+      if (!bad && sp.item >= 0) {
+        t = items[sp.item].t;
+        h = items[sp.item].h;
+        w = items[sp.item].w;
+        bad = t < 0 || h < 0 || w < 0 || h % merge || w % merge || (h > 0 && w > 0 && t * h > 0x7fffffffLL / w);
+        h /= merge;
+        w /= merge;
+      }
+      long long words = sp.text;
+      if (bad) {
+        t = h = w = words = 0;
+        atomicMin(&first_bad, ((unsigned)i << 4) | (unsigned)kDesc);
+      }
+      const long long seen = t * h * w;
+      long long reach = 0;
+      if (seen > 0) {
+        reach = (t - 1) * sp.step + 1;
+        reach = reach > h ? reach : h;
+        reach = reach > w ? reach : w;
+      }
+      text[i] = (int)words;
+      step[i] = sp.step;
+      height[i] = (int)(seen > 0 ? h : 0);
+      wide[i] = (int)(seen > 0 ? w : 0);
+      e = SpanScan{words + seen, words + reach, sp.first != 0};
+    }
+    const SpanScan own = e;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      SpanScan o;
+      o.tokens = __shfl_up_sync(0xffffffffu, e.tokens, d);
+      o.reach = __shfl_up_sync(0xffffffffu, e.reach, d);
+      o.restart = __shfl_up_sync(0xffffffffu, e.restart, d);
+      if (lane >= d) e = scan_join(o, e);
+    }
+    if (lane == 31) warp_total[warp] = e;
+    __syncthreads();
+    SpanScan before = carry;
+    for (int w = 0; w < warp; ++w) before = scan_join(before, warp_total[w]);
+    e = scan_join(before, e);
+    for (int w = 0; w < kThreads / 32; ++w) carry = scan_join(carry, warp_total[w]);
+    __syncthreads();
+    if (i < n) {
+      const long long at = e.tokens - own.tokens, p = e.reach - own.reach;
+      start[i] = (int)(at < rows ? at : rows);
+      base[i] = (int)(p < 0x7fffffffLL ? p : 0x7fffffffLL);
+      if (e.tokens > rows || e.reach > 0x7fffffffLL) atomicMin(&first_bad, ((unsigned)i << 4) | (unsigned)kRange);
+    }
+  }
+  if (tid == 0) start[n] = (int)(carry.tokens < rows ? carry.tokens : rows);
+  __syncthreads();
+  if (status != nullptr && blockIdx.x == 0 && tid == 0) {
+    const bool bad = code == kOk && first_bad != 0xffffffffu;
+    status[0] = bad ? (int)(first_bad & 15u) : code;
+    status[1] = bad ? (int)(first_bad >> 4) : -1;
+  }
+  const int live = start[n];
+  for (int r = blockIdx.x * kThreads + tid; r < rows; r += gridDim.x * kThreads) {
+    long long p0 = -1, p1 = -1, p2 = -1;
+    if (r < live) {
+      const int s = find_item(start, n, r);
+      const int local = r - start[s] - text[s];
+      p0 = p1 = p2 = (long long)base[s] + (r - start[s]);
+      if (local >= 0) {
+        const int hw = height[s] * wide[s];
+        const int tg = local / hw, rem = local - tg * hw;
+        const int y = rem / wide[s], x = rem - y * wide[s];
+        const long long p = (long long)base[s] + text[s];
+        p0 = p + (long long)tg * step[s];
+        p1 = p + y;
+        p2 = p + x;
+      }
+    }
+    pos[r] = (int)(p0 < 0x7fffffffLL ? p0 : 0x7fffffffLL);
+    pos[(size_t)rows + r] = (int)(p1 < 0x7fffffffLL ? p1 : 0x7fffffffLL);
+    pos[2 * (size_t)rows + r] = (int)(p2 < 0x7fffffffLL ? p2 : 0x7fffffffLL);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rotation
+// ---------------------------------------------------------------------------
+struct MropeTable {
+  uint64_t turn[kMaxPairs];    // w_i / (2 pi) in units of 2^-64 turns
+  uint8_t axis[kMaxPairs];
+};
+
+struct MropeKernelArgs {
+  const int32_t* pos;
+  int rows, half, head_dim, units_q, units, groups, rest, rows_per_block;
+  float sign;
+  const void* x[2];
+  void* y[2];
+  long long x_stride[2], y_stride[2];
+};
+
+// The angle of a pair is position * w_i.  In turns of 2^-64, position * turn[i] wraps as the
+// angle does, exactly, so no position loses accuracy: the phase's top 32 bits are the angle
+// to 2^-32 turns.
+template <typename X, int V>
+__global__ void __launch_bounds__(kThreads) mrope_kernel(const MropeKernelArgs a, const __grid_constant__ MropeTable tab) {
+  extern __shared__ float cs[];                  // [rows_per_block][2][half]
+  const int r0 = blockIdx.x * a.rows_per_block;
+  const int nr = min(a.rows_per_block, a.rows - r0);
+  for (int i = threadIdx.x; i < nr * a.half; i += kThreads) {
+    const int r = i / a.half, p = i - r * a.half;
+    const int64_t at = a.pos[(size_t)tab.axis[p] * a.rows + r0 + r];
+    const uint64_t phase = (uint64_t)at * tab.turn[p];
+    const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;   // 2^-31
+    float sn, c;
+    sincospif(half_turns, &sn, &c);
+    cs[(2 * r) * a.half + p] = c;
+    cs[(2 * r + 1) * a.half + p] = sn * a.sign;
+  }
+  __syncthreads();
+  using XV = Vec<X, V>;
+  // unit: (row, head, group of V pairs), then the copied tail of each head
+  const int per_row = a.units;
+  for (int u = blockIdx.y * kThreads + threadIdx.x; u < nr * per_row; u += gridDim.y * kThreads) {
+    const int r = u / per_row;
+    int v = u - r * per_row;
+    const int which = v >= a.units_q;
+    v -= which ? a.units_q : 0;
+    const int head = v / a.groups, g = v - head * a.groups;
+    const X* x = static_cast<const X*>(a.x[which]) + (long long)(r0 + r) * a.x_stride[which] + (long long)head * a.head_dim;
+    X* y = static_cast<X*>(a.y[which]) + (long long)(r0 + r) * a.y_stride[which] + (long long)head * a.head_dim;
+    const int rot = a.half / V;
+    if (g < rot) {
+      const float* c = cs + (size_t)(2 * r) * a.half + g * V;
+      const XV va = *reinterpret_cast<const XV*>(x + g * V);
+      const XV vb = *reinterpret_cast<const XV*>(x + a.half + g * V);
+      XV ya, yb;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float fa = to_f32(va.v[e]), fb = to_f32(vb.v[e]);
+        ya.v[e] = from_f32<X>(fmaf(fa, c[e], -(fb * c[a.half + e])));
+        yb.v[e] = from_f32<X>(fmaf(fb, c[e], fa * c[a.half + e]));
+      }
+      *reinterpret_cast<XV*>(y + g * V) = ya;
+      *reinterpret_cast<XV*>(y + a.half + g * V) = yb;
+    } else {
+      const int c = 2 * a.half + (g - rot) * V;
+      *reinterpret_cast<XV*>(y + c) = *reinterpret_cast<const XV*>(x + c);
+    }
+  }
+}
+
+template <typename X, int V>
+cudaError_t launch_typed(const MropeArgs& a, const MropeTable& tab, cudaStream_t s) {
+  MropeKernelArgs k;
+  k.pos = a.pos;
+  k.rows = (int)a.rows;
+  k.half = a.rotary_dim / 2;
+  k.head_dim = a.head_dim;
+  bool moved = false;            // the tail of a head is copied only where out is elsewhere
+  for (int i = 0; i < 2; ++i) {
+    k.x[i] = a.x[i];
+    k.y[i] = a.y[i];
+    k.x_stride[i] = a.x_stride[i];
+    k.y_stride[i] = a.y_stride[i];
+    moved = moved || (a.heads[i] > 0 && a.x[i] != a.y[i]);
+  }
+  k.rest = moved ? (a.head_dim - a.rotary_dim) / V : 0;
+  k.groups = k.half / V + k.rest;
+  k.units_q = a.heads[0] * k.groups;
+  k.units = (a.heads[0] + a.heads[1]) * k.groups;
+  k.sign = a.inverse ? -1.f : 1.f;
+  if (k.units == 0) return cudaSuccess;
+  int per = (4 * kThreads + k.units - 1) / k.units;
+  const int room = 8192 / (2 * k.half);
+  per = per < 1 ? 1 : per > room ? room : per;
+  // few rows: one row per block and its heads over grid.y, so that more SMs take part
+  int ysplit = 1;
+  if (a.rows < 152 * 2) {
+    per = 1;
+    ysplit = (k.units + kThreads - 1) / kThreads;
+    ysplit = ysplit > 16 ? 16 : ysplit;
+  }
+  k.rows_per_block = per;
+  const dim3 grid((unsigned)((a.rows + per - 1) / per), (unsigned)ysplit);
+  mrope_kernel<X, V><<<grid, kThreads, (size_t)per * 2 * k.half * sizeof(float), s>>>(k, tab);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mrope_apply(const MropeArgs& a, cudaStream_t s) {
+  if (a.rows == 0) return cudaSuccess;
+  MropeTable tab{};
+  const int half = a.rotary_dim / 2;
+  const double ratio = std::pow((double)a.theta, -2.0 / a.rotary_dim);
+  double w = 0.15915494309189535;               // 1 / (2 pi)
+  for (int i = 0; i < half; ++i) {
+    // turns below 1; the whole part of a larger frequency (theta < 1) turns nothing
+    tab.turn[i] = (uint64_t)std::ldexp(w - std::floor(w), 64);
+    tab.axis[i] = a.axis_of_pair[i];
+    w *= ratio;
+  }
+  // 8 elements (16 bytes) of a 16-bit type where halves, heads, rows and bases allow it, else 4
+  bool wide = a.dtype != VITFE_F32 && half % 8 == 0;
+  for (int i = 0; i < 2; ++i)
+    if (a.heads[i] > 0)
+      wide = wide && reinterpret_cast<uintptr_t>(a.x[i]) % 16 == 0 && reinterpret_cast<uintptr_t>(a.y[i]) % 16 == 0 &&
+             a.x_stride[i] % 8 == 0 && a.y_stride[i] % 8 == 0;
+  switch (a.dtype) {
+    case VITFE_BF16:
+      return wide ? launch_typed<__nv_bfloat16, 8>(a, tab, s) : launch_typed<__nv_bfloat16, 4>(a, tab, s);
+    case VITFE_F16: return wide ? launch_typed<__half, 8>(a, tab, s) : launch_typed<__half, 4>(a, tab, s);
+    default: return launch_typed<float, 4>(a, tab, s);
+  }
+}
+
+cudaError_t launch_mrope_positions(const vitfe_span* spans, const int32_t* n_spans, int max_spans,
+                                   const vitfe_item* items, const int32_t* n_items, int max_items, int merge,
+                                   int64_t rows, int32_t* pos, int32_t* status, cudaStream_t s) {
+  int64_t blocks = (rows + kThreads - 1) / kThreads;
+  blocks = blocks < 1 ? 1 : blocks > 608 ? 608 : blocks;
+  mrope_positions_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(spans, n_spans, max_spans, items, n_items, max_items,
+                                                               merge, (int)rows, pos, status);
+  return cudaGetLastError();
+}
+
+}  // namespace vitfe

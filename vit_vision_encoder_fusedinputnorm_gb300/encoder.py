@@ -1,0 +1,412 @@
+"""Torch-side calls of the encoder-block operators: layer norm, multi-axis rotary, attention.
+
+What runs behind the front end's embeddings: the tower's norms and packed attention
+(sequence boundaries from ``FrontEnd.cu_seqlens``) and the language model's rotary positions of
+text, images and video.  PyTorch provides device memory and streams; every operator runs in the
+library's CUDA kernels (see ``binding``).
+
+The plain functions return gradients explicitly.  ``LayerNorm``, ``MropeRotation`` and
+``PackedAttention`` are the same calls as torch autograd functions, and ``EncoderBlock`` is a
+pre-norm transformer block made of them.
+
+A call runs on the current stream, or on ``stream`` (a torch stream or a cudaStream_t), and what it
+allocates belongs to that stream.  A tensor made on another stream has to be ready there, as for
+any other call.
+"""
+from __future__ import annotations
+
+import functools
+from typing import Optional, Sequence, Tuple
+
+import torch
+
+from . import binding as B
+
+_DTYPES = {torch.bfloat16: B.VITFE_BF16, torch.float16: B.VITFE_F16, torch.float32: B.VITFE_F32}
+
+
+def _dtype(t: torch.Tensor) -> int:
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"bfloat16, float16 or float32 tensors are supported, not {t.dtype}") from None
+
+
+def _on(x: torch.Tensor, stream):
+    return stream if stream is not None else torch.cuda.current_stream(x.device)
+
+
+def _stream_call(fn):
+    """Run fn with ``stream`` current, so that outputs and workspaces are that stream's memory."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kwargs)
+    return call
+
+
+def _need_cuda(*tensors) -> None:
+    first = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("CUDA tensors are needed")
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            raise ValueError("all tensors have to be on one device")
+
+
+def _rows(x: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, width, row stride) of a [rows][width] tensor whose rows are contiguous."""
+    if x.dim() != 2:
+        raise ValueError(f"{name}: a [rows][width] tensor is needed, not {tuple(x.shape)}")
+    if x.shape[0] and x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: its rows have to be contiguous")
+    stride = x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return x.shape[0], x.shape[1], stride
+
+
+def _heads(x: torch.Tensor, name: str) -> int:
+    """Row stride of a [rows][heads][head_dim] tensor whose rows are contiguous."""
+    if x.dim() != 3:
+        raise ValueError(f"{name}: a [rows][heads][head_dim] tensor is needed, not {tuple(x.shape)}")
+    if x.shape[0] and ((x.shape[2] > 1 and x.stride(2) != 1) or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+        raise ValueError(f"{name}: its rows have to be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _like(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _vector(v: Optional[torch.Tensor], width: int, name: str, dtype: Optional[torch.dtype] = None):
+    if v is None:
+        return
+    if v.shape != (width,) or not v.is_contiguous() or (dtype is not None and v.dtype != dtype):
+        raise ValueError(f"{name}: a contiguous [{width}] tensor{f' of {dtype}' if dtype else ''} is needed")
+
+
+# ------------------------------------------------------------------ layer norm
+
+@_stream_call
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stats: bool = False, stream=None):
+    """Layer norm over the rows of x [rows][width]; with ``stats``: (y, mean, rstd) for the backward pass."""
+    rows, width, stride = _rows(x, "x")
+    _need_cuda(x, weight, bias, out)
+    _vector(weight, width, "weight")
+    _vector(bias, width, "bias", None if weight is None else weight.dtype)
+    if out is None:
+        out = _like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out: x's shape and type are needed")
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    params = weight if weight is not None else bias
+    with torch.cuda.device(x.device):
+        B.vitfe_layer_norm(x, stride, _dtype(x), rows, width, weight, bias,
+                           B.VITFE_F32 if params is None else _dtype(params), eps, out, _rows(out, "out")[2], mean,
+                           rstd, _on(x, stream))
+    return (out, mean, rstd) if stats else out
+
+
+@_stream_call
+def layer_norm_backward(dout, x, mean, rstd, weight=None, params: bool = True, stream=None):
+    """(dx, dweight, dbias) of layer_norm; the last two float32, or None without ``params``."""
+    rows, width, stride = _rows(x, "x")
+    _need_cuda(dout, x, mean, rstd, weight)
+    if dout.shape != x.shape or dout.dtype != x.dtype:
+        raise ValueError("dout: x's shape and type are needed")
+    _vector(weight, width, "weight")
+    _vector(mean, rows, "mean", torch.float32)
+    _vector(rstd, rows, "rstd", torch.float32)
+    dx = _like(x)
+    dweight = dbias = work = None
+    size = 0
+    if params:
+        dweight = torch.empty(width, dtype=torch.float32, device=x.device)
+        dbias = torch.empty(width, dtype=torch.float32, device=x.device)
+        size = B.vitfe_layer_norm_workspace(rows, width)
+        work = torch.empty(size, dtype=torch.uint8, device=x.device)
+    with torch.cuda.device(x.device):
+        B.vitfe_layer_norm_backward(dout, _rows(dout, "dout")[2], x, stride, _dtype(x), rows, width, weight,
+                                    B.VITFE_F32 if weight is None else _dtype(weight), mean, rstd, dx, width, dweight,
+                                    dbias, work, size, _on(x, stream))
+    return dx, dweight, dbias
+
+
+# ------------------------------------------------------------------ rotary positions
+
+def section_axes(sections: Sequence[int], interleaved: bool = False) -> list:
+    """The axis of each rotated pair, for sections of (time, height, width, ...) pairs.
+
+    In order: the first section's pairs, then the second's, and so on.  Interleaved: axis a > 0
+    takes the pairs a, a + n, a + 2n, ... (n axes) until its section is used up, axis 0 the rest.
+    """
+    n, total = len(sections), sum(sections)
+    if not interleaved:
+        return [a for a in range(n) for _ in range(sections[a])]
+    return [i % n if i % n and i < n * sections[i % n] else 0 for i in range(total)]
+
+
+@_stream_call
+def mrope_positions(spans, n_spans, items, n_items, rows: int, merge: int = 2, pos=None, status=None, stream=None):
+    """int32 [3][rows] positions of a packed prompt (vitfe_mrope_positions).
+
+    spans: int32 [capacity][4] on the device (first, text, item, step); items: the item table of
+    ``FrontEnd.upload`` (24 bytes an item), or None.
+    """
+    _need_cuda(spans, n_spans, items, n_items, pos, status)
+    if spans.dtype != torch.int32 or spans.dim() != 2 or spans.shape[1] != 4 or not spans.is_contiguous():
+        raise ValueError("spans: a contiguous int32 [capacity][4] tensor is needed")
+    if n_spans.dtype != torch.int32 or (n_items is not None and n_items.dtype != torch.int32):
+        raise ValueError("n_spans, n_items: int32 tensors are needed")
+    capacity = 0
+    if items is not None:
+        if not items.is_contiguous():
+            raise ValueError("items: a contiguous table is needed")
+        capacity = items.numel() * items.element_size() // 24
+    if pos is None:
+        pos = torch.empty((3, rows), dtype=torch.int32, device=spans.device)
+    elif pos.shape != (3, rows) or pos.dtype != torch.int32 or not pos.is_contiguous():
+        raise ValueError("pos: a contiguous int32 [3][rows] tensor is needed")
+    with torch.cuda.device(spans.device):
+        B.vitfe_mrope_positions(spans, n_spans, spans.shape[0], items, n_items, capacity, merge, rows, pos, status,
+                                _on(spans, stream))
+    return pos
+
+
+@_stream_call
+def mrope_apply(q, k, pos, axes: Sequence[int], theta: float = 10000.0, inverse: bool = False, q_out=None, k_out=None,
+                stream=None):
+    """(q, k) rotated: [rows][heads][head_dim] each, either may be None.
+
+    pos: int32 [n axes][rows]; axes: the axis of each pair (``section_axes``), rotary_dim / 2 of
+    them.  q_out, k_out: where to write (q and k themselves for in place), else new tensors.
+    """
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is needed")
+    _need_cuda(q, k, pos, q_out, k_out)
+    if k is not None and (k.dtype != x.dtype or k.shape[0] != x.shape[0] or k.shape[2] != x.shape[2]):
+        raise ValueError("q and k: the same rows, head_dim and type are needed")
+    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[1] != x.shape[0] or not pos.is_contiguous():
+        raise ValueError("pos: a contiguous int32 [axes][rows] tensor is needed")
+
+    def target(x, out, name):
+        if x is None:
+            return None, 0, 0, None, 0
+        out = _like(x) if out is None else out
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError(f"{name}: the input's shape and type are needed")
+        return x, x.shape[1], _heads(x, name), out, _heads(out, name)
+
+    tq, tk = target(q, q_out, "q_out"), target(k, k_out, "k_out")
+    with torch.cuda.device(x.device):
+        B.vitfe_mrope_apply(pos, pos.shape[0], bytes(axes), 2 * len(axes), theta, inverse, x.shape[0], x.shape[2],
+                            _dtype(x), *tq, *tk, _on(x, stream))
+    return tq[3], tk[3]
+
+
+# ------------------------------------------------------------------ attention
+
+class AttentionPlan:
+    """Sequence boundaries of a batch, made into the attention kernels' work list once for all layers.
+
+    cu_q, cu_k: int32 [sequences + 1] on the device (``FrontEnd.cu_seqlens`` gives them; the tower's
+    queries and keys share one).  rows_q, rows_k: rows of q and of k, v, padding included.
+    """
+
+    @_stream_call
+    def __init__(self, cu_q, cu_k, rows_q: int, rows_k: int, heads_q: int, heads_kv: int, head_dim: int,
+                 causal: bool = False, status=None, stream=None):
+        _need_cuda(cu_q, cu_k, status)
+        for c in (cu_q, cu_k):
+            if c.dtype != torch.int32 or c.dim() != 1 or not c.is_contiguous() or c.shape != cu_q.shape or not len(c):
+                raise ValueError("cu_q, cu_k: contiguous int32 [sequences + 1] tensors of one length are needed")
+        self.shape = B.AttentionShape(rows_q, rows_k, len(cu_q) - 1, heads_q, heads_kv, head_dim, int(causal),
+                                      B.VITFE_BF16)
+        self.device = cu_q.device
+        size = B.vitfe_attention_plan_bytes(self.shape)
+        self.buffer = torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
+        self.update(cu_q, cu_k, status, stream=stream)
+
+    @_stream_call
+    def update(self, cu_q, cu_k, status=None, stream=None) -> None:
+        """Plan new boundaries in the same buffer (the shape stays: a captured graph replays this)."""
+        with torch.cuda.device(self.device):
+            B.vitfe_attention_plan(self.shape, cu_q, cu_k, self.buffer, status, _on(cu_q, stream))
+
+    def of(self, q, k, v) -> "B.AttentionShape":
+        """The shape of a call with these tensors; raises where they do not fit the plan."""
+        s = self.shape
+        if q.dim() != 3 or q.shape != (s.rows_q, s.heads_q, s.head_dim):
+            raise ValueError(f"q: {(s.rows_q, s.heads_q, s.head_dim)} is planned, not {tuple(q.shape)}")
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dim() != 3 or t.shape != (s.rows_k, s.heads_kv, s.head_dim):
+                raise ValueError(f"{name}: {(s.rows_k, s.heads_kv, s.head_dim)} is planned, not {tuple(t.shape)}")
+            if t.dtype != q.dtype:
+                raise ValueError("q, k, v: one type is needed")
+        if q.device != self.device:
+            raise ValueError("the plan is on another device")
+        return B.AttentionShape(s.rows_q, s.rows_k, s.max_seqs, s.heads_q, s.heads_kv, s.head_dim, s.causal, _dtype(q))
+
+
+def _work(size: int, device):
+    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+
+
+@_stream_call
+def attention(q, k, v, plan: AttentionPlan, scale: Optional[float] = None, lse: bool = False, out=None, status=None,
+              stream=None):
+    """softmax(scale q k^T) v over the plan's sequences; with ``lse``: (out, lse float32 [rows][heads])."""
+    _need_cuda(q, k, v, out, status)
+    shape = plan.of(q, k, v)
+    if out is None:
+        out = _like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out: q's shape and type are needed")
+    sums = torch.empty((shape.rows_q, shape.heads_q), dtype=torch.float32, device=q.device) if lse else None
+    with torch.cuda.device(q.device):
+        B.vitfe_attention(shape, plan.buffer, q, _heads(q, "q"), k, _heads(k, "k"), v, _heads(v, "v"),
+                          shape.head_dim ** -0.5 if scale is None else scale, out, _heads(out, "out"), sums,
+                          _work(B.vitfe_attention_workspace(shape), q.device), status, _on(q, stream))
+    return (out, sums) if lse else out
+
+
+@_stream_call
+def attention_backward(dout, q, k, v, out, lse, plan: AttentionPlan, scale: Optional[float] = None, status=None,
+                       stream=None):
+    """(dq, dk, dv) of attention; ``out`` and ``lse`` are the forward pass's."""
+    _need_cuda(dout, q, k, v, out, lse, status)
+    shape = plan.of(q, k, v)
+    for t, name in ((dout, "dout"), (out, "out")):
+        if t.shape != q.shape or t.dtype != q.dtype:
+            raise ValueError(f"{name}: q's shape and type are needed")
+    if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse: the forward pass's float32 [rows][heads] is needed")
+    dq, dk, dv = _like(q), _like(k), _like(v)
+    with torch.cuda.device(q.device):
+        B.vitfe_attention_backward(shape, plan.buffer, dout, _heads(dout, "dout"), q, _heads(q, "q"), k,
+                                   _heads(k, "k"), v, _heads(v, "v"), out, _heads(out, "out"), lse,
+                                   shape.head_dim ** -0.5 if scale is None else scale, dq, _heads(dq, "dq"), dk,
+                                   _heads(dk, "dk"), dv, _heads(dv, "dv"),
+                                   _work(B.vitfe_attention_backward_workspace(shape), q.device), status,
+                                   _on(q, stream))
+    return dq, dk, dv
+
+
+# ------------------------------------------------------------------ autograd
+
+class LayerNorm(torch.autograd.Function):
+    """``LayerNorm.apply(x, weight, bias, eps)``: layer_norm with its gradients."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = layer_norm(x, weight, bias, eps, stats=True)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        params = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+        dx, dw, db = layer_norm_backward(dy.contiguous(), x, mean, rstd, weight, params=params)
+        return (dx, dw.to(weight.dtype) if ctx.needs_input_grad[1] else None,
+                db.to(ctx.bias_dtype) if ctx.needs_input_grad[2] else None, None)
+
+
+class MropeRotation(torch.autograd.Function):
+    """``MropeRotation.apply(q, k, pos, axes, theta)``: mrope_apply; its gradient is the inverse rotation."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, axes, theta):
+        ctx.save_for_backward(pos)
+        ctx.axes, ctx.theta = axes, theta
+        return mrope_apply(q, k, pos, axes, theta)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        dq, dk = mrope_apply(dq.contiguous(), dk.contiguous(), ctx.saved_tensors[0], ctx.axes, ctx.theta, inverse=True)
+        return dq, dk, None, None, None
+
+
+class TableRotation(torch.autograd.Function):
+    """``TableRotation.apply(x, cos, sin)``: vitfe_rope_apply with the tower's tables, out of place."""
+
+    @staticmethod
+    def _turn(x, cos, sin):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device).copy_(x)
+        with torch.cuda.device(x.device):
+            B.vitfe_rope_apply(cos, sin, x.shape[0], x.shape[2], y, x.shape[1], _heads(y, "x"), None, 0, 0,
+                               torch.cuda.current_stream(x.device))
+        return y
+
+    @staticmethod
+    def forward(ctx, x, cos, sin):
+        ctx.save_for_backward(cos, sin)
+        return TableRotation._turn(x, cos, sin)
+
+    @staticmethod
+    def backward(ctx, dy):
+        cos, sin = ctx.saved_tensors
+        return TableRotation._turn(dy, cos, -sin), None, None
+
+
+class PackedAttention(torch.autograd.Function):
+    """``PackedAttention.apply(q, k, v, plan, scale)``: attention with its gradients."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, plan, scale):
+        out, lse = attention(q, k, v, plan, scale, lse=True)
+        ctx.save_for_backward(q, k, v, out, lse)
+        ctx.plan, ctx.scale = plan, scale
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse = ctx.saved_tensors
+        dq, dk, dv = attention_backward(dout.contiguous(), q, k, v, out, lse, ctx.plan, ctx.scale)
+        return dq, dk, dv, None, None
+
+
+class EncoderBlock(torch.nn.Module):
+    """A pre-norm transformer block of the vision tower, on packed rows.
+
+    x + proj(attention(rotate(q), rotate(k), v)), then x + mlp: the rows are the front end's
+    embeddings, cos and sin its RoPE tables, and the plan is made of its ``cu_seqlens``.  The
+    projections are torch's matrix products; norms, rotation and attention are the library's.
+    """
+
+    def __init__(self, hidden: int, heads: int, mlp: int, eps: float = 1e-6, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        if hidden % heads or (hidden // heads) % 8:
+            raise ValueError("hidden has to be heads times a multiple of 8")
+        self.heads, self.eps = heads, eps
+        kw = {"dtype": dtype, "device": device}
+        self.norm1_weight = torch.nn.Parameter(torch.ones(hidden, **kw))
+        self.norm1_bias = torch.nn.Parameter(torch.zeros(hidden, **kw))
+        self.norm2_weight = torch.nn.Parameter(torch.ones(hidden, **kw))
+        self.norm2_bias = torch.nn.Parameter(torch.zeros(hidden, **kw))
+        self.qkv = torch.nn.Linear(hidden, 3 * hidden, **kw)
+        self.proj = torch.nn.Linear(hidden, hidden, **kw)
+        self.fc1 = torch.nn.Linear(hidden, mlp, **kw)
+        self.fc2 = torch.nn.Linear(mlp, hidden, **kw)
+
+    def forward(self, x, cos, sin, plan: AttentionPlan):
+        rows, hidden = x.shape
+        h = LayerNorm.apply(x, self.norm1_weight, self.norm1_bias, self.eps)
+        q, k, v = self.qkv(h).view(rows, 3 * self.heads, hidden // self.heads).split(self.heads, dim=1)
+        q, k = TableRotation.apply(q, cos, sin), TableRotation.apply(k, cos, sin)
+        a = PackedAttention.apply(q, k, v, plan, None)
+        x = x + self.proj(a.reshape(rows, hidden))
+        h = LayerNorm.apply(x, self.norm2_weight, self.norm2_bias, self.eps)
+        return x + self.fc2(torch.nn.functional.gelu(self.fc1(h), approximate="tanh"))
