@@ -223,70 +223,392 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
 }
 
 // ---------------------------------------------------------------------------
-// forward: a warp per query row
+// forward
 // ---------------------------------------------------------------------------
+// One CTA per SM works through (item, key head) pairs.  An item has up to two score tiles of 128
+// rows (rows = tokens x the query heads of the key head, token-major), so that the tensor core
+// runs one tile's products while the other tile's probabilities are computed.
+//   warps 0-3, 4-7: softmax of tile 0, 1: thread = row.  Reads S from tensor memory, keeps the
+//     running maximum and sum in registers, writes P (16-bit) over S, rescales O when its
+//     reference maximum has to move, and stores the finished rows.
+//   warp 8: TMA loads of Q tiles and of the ring of K and V blocks.
+//   warp 9: the matrix instructions: S_t = Q_t K^T, O_t += P_t V.
+// Tensor memory: S0, S1 (128 columns each; P_t in the first 64 of them), O0, O1 (128 each).
+__global__ void status_ok_kernel(int32_t* status) {
+  status[0] = kOk;
+  status[1] = -1;
+}
+
+constexpr int kFwdThreads = 384;
+constexpr int kMaxStages = 10;
+constexpr int kSmemMax = 227 * 1024;
+
+struct FwdShared {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+// Key blocks [kb, kb + n) that tile t of an item reads (0: the tile has no row that sees a key).
+__device__ __forceinline__ int tile_blocks(const AttnItem& it, int t, int tok, bool causal) {
+  const int have = min(tok, it.qn - t * tok);
+  if (have <= 0) return 0;
+  const int last = causal ? min(it.kn, max(0, it.off + t * tok + have)) : it.kn;
+  return max(0, min(it.ke, ceil_div(last, kAttnKeys)) - it.kb);
+}
+
+// The w-th of this CTA's works: the list is sorted longest first and dealt back and forth, so
+// that the SMs' sums come out even.
+__device__ __forceinline__ int deal(int round) {
+  return round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(256) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v, int stages) {
+  extern __shared__ uint8_t raw[];
+  __shared__ FwdShared sh;
+  const uint32_t tiles = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim, tok = a.l.tok;
+  const bool causal = a.s.causal != 0;
+  const int nb = (d + kColBlock - 1) / kColBlock;            // column blocks of a head
+  const uint32_t tile_bytes = (uint32_t)nb * kColBlockBytes;
+  const uint32_t ring = tiles + 2 * tile_bytes;
+  volatile int* abort_flag = &sh.abort;
+  if (threadIdx.x == 0) {
+    if (a.status != nullptr && blockIdx.x == 0) {      // a wait that runs out overrides it later
+      a.status[0] = kOk;
+      a.status[1] = -1;
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&sh.q_full[t]), 1);
+      mbar_init(smem_u32(&sh.q_empty[t]), 1);
+      mbar_init(smem_u32(&sh.s_full[t]), 1);
+      mbar_init(smem_u32(&sh.p_full[t]), 4);
+      mbar_init(smem_u32(&sh.o_full[t]), 1);
+    }
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(smem_u32(&sh.kv_full[i]), 1);
+      mbar_init(smem_u32(&sh.kv_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
   const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
   const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim;
-  const int slot_rows = (int)((a.s.rows_q < 2 * a.l.tok ? a.s.rows_q : 2 * a.l.tok) * g);
-  if (a.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
-    a.status[0] = kOk;
-    a.status[1] = -1;
+  const int works = hdr->n_items * hk;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax and output
+    const int t = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + (uint32_t)t * 128u;
+    const uint32_t o_col = tmem + lanes + 256u + (uint32_t)t * 128u;
+    const int my_tok = t * tok + row / g, head_in = row % g;
+    const float scale2 = a.scale * 1.4426950408889634f;      // exponents of 2
+    const int slot_rows = (int)((a.s.rows_q < 2 * tok ? a.s.rows_q : 2 * tok) * g);
+    float2* stat = static_cast<float2*>(a.workspace);
+    float* part = reinterpret_cast<float*>(stat + a.l.cap_slots * hk * (int64_t)slot_rows);
+    uint32_t ns = 0, no = 0;                                 // phases of s_full, o_full
+    bool ok = true;
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnItem it = items[w / hk];
+      const int kh = w % hk;
+      if (it.qn <= t * tok) continue;
+      const int n = tile_blocks(it, t, tok, causal);
+      const bool live = row < tok * g && my_tok < it.qn;
+      int lim = causal ? min(it.kn, it.off + my_tok + 1) : it.kn;   // keys that the row sees
+      if (!live) lim = 0;
+      float m = -INFINITY, l = 0.f;                          // m: the reference of the exponents
+      for (int j = 0; j < n; ++j, ++ns) {
+        if (!mbar_wait_warp<false>(smem_u32(&sh.s_full[t]), ns & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_col + 32u * c, sr[c]);
+        tmem_wait_ld();
+        const int left = lim - (it.kb + j) * kAttnKeys;
+        if (__any_sync(0xffffffffu, left < kAttnKeys)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= left) sr[c][e] = 0xff800000u;   // -inf: weighs 0, whatever was there
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][e]));
+        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        // The exponents' reference moves only when the maximum has outgrown it by 2^8: until then
+        // P is at most 2^8 and the fp32 sums hold it exactly as well, and O need not be touched.
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, (top - m) * scale2 > 8.0f)) {
+          const float f = top == -INFINITY ? 1.f : exp2_approx((m - top) * scale2);
+          m = top;
+          l *= f;
+          // s_full of this block also says that the product before it is in O
+          for (int c = 0; c < d; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(o_col + (uint32_t)c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x16(o_col + (uint32_t)c, o);
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -(m * scale2);
+        const uint64_t sc = f32x2(scale2, scale2), off = f32x2(neg, neg);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t x = fma_f32x2(f32x2(__uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1])), sc, off);
+            const float p0 = exp2_approx(lo_f32(x)), p1 = exp2_approx(hi_f32(x));
+            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(p0, p1));
+            // the row sums are of the unrounded p; P is rounded for the product, as its type asks
+            sr[c][e >> 1] = pack2<T>(p0, p1);
+          }
+          tmem_st_32x32b_x16(s_col + 16u * c, sr[c]);
+        }
+        const uint64_t both = add_f32x2(sum[0], sum[1]);
+        l += lo_f32(both) + hi_f32(both);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t]));
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!mbar_wait_warp<false>(smem_u32(&sh.o_full[t]), no & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        ++no;
+        tc_fence_after();
+      }
+      const float m2 = m == -INFINITY ? -INFINITY : m * scale2;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int head = kh * g + head_in;
+      const int64_t qrow = (int64_t)it.q0 + my_tok;
+      const int64_t at = ((int64_t)max(it.slot, 0) * hk + kh) * slot_rows + my_tok * g + head_in;
+      for (int c = 0; c < d; c += 16) {
+        uint32_t o[16];
+        if (n > 0) {
+          tmem_ld_32x32b_x16(o_col + (uint32_t)c, o);
+          tmem_wait_ld();
+        }
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+        if (!live) continue;
+        if (it.slot < 0) {
+          T* out = static_cast<T*>(a.out) + qrow * a.out_stride + head * d + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            if (c + e < d)
+              *reinterpret_cast<uint4*>(out + e) = make_uint4(pack2<T>(f[e], f[e + 1]), pack2<T>(f[e + 2], f[e + 3]),
+                                                              pack2<T>(f[e + 4], f[e + 5]), pack2<T>(f[e + 6], f[e + 7]));
+        } else {
+          float* out = part + at * d + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            if (c + e < d) *reinterpret_cast<float4*>(out + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        }
+      }
+      tc_fence_before();
+      if (live) {
+        if (it.slot >= 0) stat[at] = make_float2(m2, l);
+        else if (a.lse) a.lse[qrow * a.s.heads_q + head] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------- loads
+    if (lane == 0) {
+      uint32_t nq[2] = {0, 0}, nk = 0;
+      bool ok = true;
+      const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
+      auto load = [&](const CUtensorMap* map, int head, int key) {
+        const uint32_t st = nk % (uint32_t)stages, ph = (nk / (uint32_t)stages) & 1u;
+        if (!mbar_wait(smem_u32(&sh.kv_empty[st]), ph ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        const uint32_t bar = smem_u32(&sh.kv_full[st]);
+        mbar_arrive_expect_tx(bar, tile_bytes);
+        for (int b = 0; b < nb; ++b)
+          tma_load_3d(ring + st * tile_bytes + (uint32_t)b * kColBlockBytes, map, bar, b * kColBlock, head, key);
+        ++nk;
+        return true;
+      };
+      auto load_q = [&](const AttnItem& it, int kh, int t) {
+        const uint32_t bar = smem_u32(&sh.q_full[t]);
+        if (!mbar_wait(smem_u32(&sh.q_empty[t]), (nq[t] & 1u) ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        mbar_arrive_expect_tx(bar, q_bytes);
+        for (int b = 0; b < nb; ++b)
+          tma_load_3d(tiles + (uint32_t)t * tile_bytes + (uint32_t)b * kColBlockBytes, &map_q, bar, b * kColBlock,
+                      kh * g, it.q0 + t * tok);
+        ++nq[t];
+        return true;
+      };
+      for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+        const AttnItem it = items[w / hk];
+        const int kh = w % hk;
+        const int n0 = tile_blocks(it, 0, tok, causal), n1 = tile_blocks(it, 1, tok, causal);
+        const int n = max(n0, n1);
+        if (n0 > 0) ok = load_q(it, kh, 0);
+        if (ok && n > 0) ok = load(&map_k, kh, it.k0 + it.kb * kAttnKeys);
+        if (ok && n1 > 0) ok = load_q(it, kh, 1);
+        for (int j = 0; ok && j < n; ++j) {
+          ok = load(&map_v, kh, it.k0 + (it.kb + j) * kAttnKeys);
+          if (ok && j + 1 < n) ok = load(&map_k, kh, it.k0 + (it.kb + j + 1) * kAttnKeys);
+        }
+      }
+      if (*abort_flag) {
+        // this warp's last loads land on their own; wait for them before the CTA ends
+        const uint64_t t0 = global_timer_ns();
+        for (int t = 0; t < 2; ++t)
+          while (nq[t] > 0 && !mbar_try_wait(smem_u32(&sh.q_full[t]), (nq[t] - 1) & 1u) &&
+                 global_timer_ns() - t0 < kAttnWaitNs) {
+          }
+        const uint32_t back = nk < (uint32_t)stages ? nk : (uint32_t)stages;
+        for (uint32_t i = nk - back; i < nk; ++i)
+          while (!mbar_try_wait(smem_u32(&sh.kv_full[i % (uint32_t)stages]), (i / (uint32_t)stages) & 1u) &&
+                 global_timer_ns() - t0 < kAttnWaitNs) {
+          }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------- matrix instructions
+    const uint32_t id_s = idesc_16<T>(128, kAttnKeys, false);
+    const uint32_t id_o = idesc_16<T>(128, (d + 15) / 16 * 16, true);
+    const int ksteps = (d + 15) / 16;
+    uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nk = 0;
+    bool ok = true;
+    auto stage_of = [&](uint32_t i) { return i % (uint32_t)stages; };
+    auto wait_kv = [&](uint32_t i) {
+      if (!mbar_wait_warp<false>(smem_u32(&sh.kv_full[stage_of(i)]), (i / (uint32_t)stages) & 1u, abort_flag, kAttnWaitNs))
+        ok = false;
+      return ok;
+    };
+    auto scores = [&](int t, uint32_t kst) {      // S_t = Q_t K^T, announced on s_full
+      if (elect_one()) {
+        const uint64_t qd = sw128_desc(tiles + (uint32_t)t * tile_bytes), kd = sw128_desc(ring + kst * tile_bytes);
+        for (int k = 0; k < ksteps; ++k) {
+          const uint64_t o = (uint64_t)((k >> 2) * (kColBlockBytes >> 4) + (k & 3) * 2);
+          umma_bf16(tmem + (uint32_t)t * 128u, qd + o, kd + o, id_s, k > 0);
+        }
+        umma_commit(smem_u32(&sh.s_full[t]));
+      }
+      __syncwarp();
+    };
+    auto output = [&](int t, uint32_t vst, bool first) {      // O_t (+)= P_t V
+      if (elect_one()) {
+        const uint64_t vd = sw128_desc_rows(ring + vst * tile_bytes);
+#pragma unroll
+        for (int k = 0; k < kAttnKeys / 16; ++k)
+          umma_ta(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + 8u * k, vd + (uint64_t)(128 * k), id_o,
+                  !first || k > 0);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(smem_u32(bar));
+      __syncwarp();
+    };
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnItem it = items[w / hk];
+      const int nt[2] = {tile_blocks(it, 0, tok, causal), tile_blocks(it, 1, tok, causal)};
+      const int n = max(nt[0], nt[1]);
+      if (n == 0) continue;
+      uint32_t ik = nk, iv = nk + 1;              // ring indexes of K(j), V(j): K0 V0 K1 V1 ...
+      if (!wait_kv(ik)) break;
+      for (int t = 0; ok && t < 2; ++t) {
+        if (nt[t] == 0) continue;
+        if (!mbar_wait_warp<false>(smem_u32(&sh.q_full[t]), nq[t] & 1u, abort_flag, kAttnWaitNs)) ok = false;
+        else {
+          ++nq[t];
+          scores(t, stage_of(ik));
+          if (nt[t] == 1) commit(&sh.q_empty[t]);
+        }
+      }
+      if (!ok) break;
+      commit(&sh.kv_empty[stage_of(ik)]);
+      for (int j = 0; ok && j < n; ++j) {
+        const bool more = j + 1 < n;
+        for (int t = 0; ok && t < 2; ++t) {
+          if (j >= nt[t]) continue;
+          if (!mbar_wait_warp<false>(smem_u32(&sh.p_full[t]), np[t] & 1u, abort_flag, kAttnWaitNs)) {
+            ok = false;
+            break;
+          }
+          ++np[t];
+          tc_fence_after();
+          if (t == 0 || nt[0] <= j) {
+            if (!wait_kv(iv)) break;
+            const int have = it.kn - (it.kb + j) * kAttnKeys;   // rows past the sequence's end weigh 0 in P,
+            if (have < kAttnKeys) zero_tile_rows(ring + stage_of(iv) * tile_bytes, nb, have);   // but 0 * NaN is NaN
+          }
+          output(t, stage_of(iv), j == 0);
+          if (j + 1 == nt[t]) {
+            commit(&sh.o_full[t]);
+          } else {
+            if ((t == 0 || nt[0] <= j + 1) && !wait_kv(ik + 2)) break;
+            scores(t, stage_of(ik + 2));
+            if (j + 2 == nt[t]) commit(&sh.q_empty[t]);
+          }
+        }
+        if (!ok) break;
+        commit(&sh.kv_empty[stage_of(iv)]);
+        if (more) commit(&sh.kv_empty[stage_of(ik + 2)]);
+        ik += 2;
+        iv += 2;
+      }
+      nk += 2u * (uint32_t)n;
+    }
+    if (!ok) {      // matrix instructions in flight end on their own: wait for them
+      commit(&sh.drain);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_u32(&sh.drain), 0) && global_timer_ns() - t0 < kAttnWaitNs) {
+      }
+      __syncwarp();
+    }
   }
-  float2* stat = static_cast<float2*>(a.workspace);
-  float* part = reinterpret_cast<float*>(stat + a.l.cap_slots * hk * (int64_t)slot_rows);
-  for (int w = blockIdx.x; w < hdr->n_items * hk; w += gridDim.x) {
-    const AttnItem it = items[w / hk];
-    const int kh = w % hk;
-    for (int r = warp; r < it.qn * g; r += 8) {
-      const int tok = r / g, head = kh * g + r % g;
-      const int lim = a.s.causal ? min(it.kn, it.off + tok + 1) : it.kn;
-      const T* q = static_cast<const T*>(a.q) + (int64_t)(it.q0 + tok) * a.q_stride + head * d;
-      float fq[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fq[i] = lane + 32 * i < d ? to_f32(q[lane + 32 * i]) * a.scale : 0.f;
-      float m = -INFINITY, l = 0.f;
-      for (int j = it.kb * kAttnKeys; j < min(lim, it.ke * kAttnKeys); ++j) {
-        const T* k = static_cast<const T*>(a.k) + (int64_t)(it.k0 + j) * a.k_stride + kh * d;
-        const T* v = static_cast<const T*>(a.v) + (int64_t)(it.k0 + j) * a.v_stride + kh * d;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < d) s = fmaf(fq[i], to_f32(k[lane + 32 * i]), s);
-        s = warp_sum(s);
-        const float mn = fmaxf(m, s);
-        const float mz = mn == -INFINITY ? 0.f : mn;
-        const float c = __expf(m - mz), p = __expf(s - mz);
-        l = l * c + p;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < d) o[i] = fmaf(o[i], c, p * to_f32(v[lane + 32 * i]));
-      }
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const float lse = l > 0.f || l != l ? m + logf(l) : -INFINITY;
-      if (it.slot < 0) {
-        T* out = static_cast<T*>(a.out) + (int64_t)(it.q0 + tok) * a.out_stride + head * d;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < d) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
-        if (a.lse && lane == 0) a.lse[(int64_t)(it.q0 + tok) * a.s.heads_q + head] = lse;
-      } else {
-        const int64_t at = ((int64_t)it.slot * hk + kh) * slot_rows + r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < d) part[at * d + lane + 32 * i] = o[i] * inv;
-        if (lane == 0) stat[at] = make_float2(m, l);
-      }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && a.status != nullptr) {
+    if (sh.abort) {
+      a.status[0] = kTimeout;
+      a.status[1] = -1;
     }
   }
 }
 
-// Joins the pieces of a cut item, in their order.  A piece holds its rows' maximum m, sum l and
-// normalised output: out = sum of w_i out_i / sum of w_i, w_i = l_i exp(m_i - top).  (m and l
+// Joins the pieces of a cut item, in their order.  A piece holds its rows' maximum m (as an
+// exponent of 2), sum l and normalised output: out = sum of w_i out_i / sum of w_i,
+// w_i = l_i 2^(m_i - top).  (m and l
 // stay apart: m + log l would lose l next to a large score.)  A warp per row.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
@@ -309,7 +631,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
       for (int p = 0; p < jn.pieces; ++p) {
         const float2 ml = stat[at + p * step];
         if (ml.y == 0.f) continue;             // no key of this piece weighs anything (NaN goes on)
-        const float wgt = ml.y * __expf(ml.x - ref);
+        const float wgt = ml.y * exp2_approx(ml.x - ref);
         sum += wgt;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -322,15 +644,35 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
       for (int i = 0; i < 4; ++i)
         if (lane + 32 * i < d) out[lane + 32 * i] = from_f32<T>(o[i] * inv);
       if (a.lse && lane == 0)
-        a.lse[(int64_t)(jn.q0 + tok) * a.s.heads_q + head] = sum == 0.f ? -INFINITY : ref + logf(sum);
+        a.lse[(int64_t)(jn.q0 + tok) * a.s.heads_q + head] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
     }
   }
 }
 
 template <typename T>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
-  const int64_t work = a.l.cap_items * a.s.heads_kv;
-  attn_kernel<T><<<(unsigned)(work < 1216 ? work : 1216), 256, 0, st>>>(a);
+  const vitfe_attention_shape& s = a.s;
+  CUtensorMap mq, mk, mv;
+  // without keys no block is ever loaded: any valid map will do
+  const bool keys = s.rows_k > 0;
+  if (!make_head_map(&mq, a.q, s.dtype, s.head_dim, s.heads_q, s.rows_q, a.q_stride, a.l.group, a.l.tok) ||
+      !make_head_map(&mk, keys ? a.k : a.q, s.dtype, s.head_dim, s.heads_kv, keys ? s.rows_k : 1,
+                     keys ? a.k_stride : a.q_stride, 1, kAttnKeys) ||
+      !make_head_map(&mv, keys ? a.v : a.q, s.dtype, s.head_dim, s.heads_kv, keys ? s.rows_k : 1,
+                     keys ? a.v_stride : a.q_stride, 1, kAttnKeys))
+    return cudaErrorInvalidValue;
+  const int tile = (s.head_dim + kColBlock - 1) / kColBlock * kColBlockBytes;
+  int stages = (kSmemMax - 2048 - 2 * tile) / tile;      // 2 KB: alignment and the barriers
+  if (stages > kMaxStages) stages = kMaxStages;
+  const int smem = (2 + stages) * tile + 1024;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t work = a.l.cap_items * s.heads_kv;
+  attn_kernel<T><<<(unsigned)(work < sms ? work : sms), kFwdThreads, smem, st>>>(a, mq, mk, mv, stages);
   if (a.l.may_split)
     attn_join_kernel<T><<<2 * kAttnSMs, 256, 0, st>>>(a);
   return cudaGetLastError();
@@ -357,7 +699,10 @@ cudaError_t launch_attention_plan(const vitfe_attention_shape& s, const int32_t*
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
-  if (a.s.rows_q == 0) return cudaSuccess;
+  if (a.s.rows_q == 0) {
+    if (a.status != nullptr) status_ok_kernel<<<1, 1, 0, st>>>(a.status);
+    return cudaGetLastError();
+  }
   return a.s.dtype == VITFE_F16 ? launch_typed<__half>(a, st) : launch_typed<__nv_bfloat16>(a, st);
 }
 

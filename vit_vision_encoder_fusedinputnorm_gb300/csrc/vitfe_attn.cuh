@@ -103,7 +103,7 @@ inline int64_t attn_workspace(const vitfe_attention_shape& s) {
   return (l.cap_slots * s.heads_kv * attn_slot_rows(s) * (s.head_dim + 2) * 4 + 15) / 16 * 16;
 }
 inline int64_t attn_backward_workspace(const vitfe_attention_shape& s) {
-  return (s.rows_q * s.heads_q * 4 + 15) / 16 * 16;   // delta
+  return (s.rows_q * s.heads_q * 8 + 15) / 16 * 16;   // two floats a row and head
 }
 
 // ---------------------------------------------------------------------------

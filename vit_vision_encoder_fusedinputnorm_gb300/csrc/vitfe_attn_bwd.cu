@@ -1,130 +1,705 @@
-// Attention over packed sequences: the backward pass.
+// Attention over packed sequences: the backward pass, in three kernels.
+//   rows: delta = sum(dout * out) and the exponents' references, per query row and head.
+//   keys: dk and dv of 128 keys, over the query tiles that see them (4 products a tile).
+//   queries: dq of 128 rows, over the key blocks that they see (3 products a block).
+// S and dP are computed in both of the last two, so that every sum has one owner: no atomics, no
+// partial results, the same bits every time, for 7 products instead of 5.
 #include "vitfe_attn.cuh"
 
 namespace vitfe {
 namespace {
 
-// dq and delta: a warp per query row.
+constexpr int kBwdThreads = 384;     // 8 warps on scores, then loads, matrix instructions, row values, idle
+constexpr int kMaxPairs = 4;         // ring stages
+constexpr int kSmemMax = 227 * 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Per query row and head: the exponents' reference and delta.  A row that sees no key (lse -inf)
+// gets +inf, so that its probabilities are 0.
+struct alignas(8) RowValue {
+  float lse2, delta;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) attn_dq_kernel(const AttnArgs a) {
-  const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
-  const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim;
-  float* delta = static_cast<float*>(a.workspace);
-  if (a.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
+__global__ void __launch_bounds__(256) attn_rows_kernel(const AttnArgs a) {
+  if (a.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {   // a wait that runs out overrides it later
     a.status[0] = kOk;
     a.status[1] = -1;
   }
-  for (int w = blockIdx.x; w < hdr->n_items * hk; w += gridDim.x) {
-    const AttnItem it = items[w / hk];
-    if (it.kb > 0) continue;               // the first piece of a cut item takes all of it
-    const int kh = w % hk;
-    for (int r = warp; r < it.qn * g; r += 8) {
-      const int tok = r / g, head = kh * g + r % g;
-      const int lim = a.s.causal ? min(it.kn, it.off + tok + 1) : it.kn;
-      const int64_t row = it.q0 + tok;
-      const T* q = static_cast<const T*>(a.q) + row * a.q_stride + head * d;
-      const T* od = static_cast<const T*>(a.out) + row * a.out_stride + head * d;
-      const T* dd = static_cast<const T*>(a.dout) + row * a.dout_stride + head * d;
-      float fq[4], fd[4], dq[4] = {0.f, 0.f, 0.f, 0.f}, dl = 0.f;
+  // 16 lanes per (row, head), 8 elements a lane
+  const int d = a.s.head_dim, sub = threadIdx.x & 15;
+  const int64_t n = a.s.rows_q * a.s.heads_q, step = (int64_t)gridDim.x * 16;
+  RowValue* rows = static_cast<RowValue*>(a.workspace);
+  for (int64_t i0 = (int64_t)blockIdx.x * 16; i0 < n; i0 += step) {
+    const int64_t i = i0 + (threadIdx.x >> 4);
+    float s = 0.f;
+    if (i < n && sub * 8 < d) {
+      const int64_t r = i / a.s.heads_q;
+      const int h = (int)(i - r * a.s.heads_q);
+      const Vec<T, 8> o = *reinterpret_cast<const Vec<T, 8>*>(static_cast<const T*>(a.out) + r * a.out_stride + h * d + sub * 8);
+      const Vec<T, 8> g = *reinterpret_cast<const Vec<T, 8>*>(static_cast<const T*>(a.dout) + r * a.dout_stride + h * d + sub * 8);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in = lane + 32 * i < d;
-        fq[i] = in ? to_f32(q[lane + 32 * i]) * a.scale : 0.f;
-        fd[i] = in ? to_f32(dd[lane + 32 * i]) : 0.f;
-        if (in) dl = fmaf(fd[i], to_f32(od[lane + 32 * i]), dl);
-      }
-      dl = warp_sum(dl);
-      if (lane == 0) delta[row * a.s.heads_q + head] = dl;
-      const float lse = a.lse[row * a.s.heads_q + head];
-      for (int j = 0; j < lim; ++j) {
-        const T* k = static_cast<const T*>(a.k) + (int64_t)(it.k0 + j) * a.k_stride + kh * d;
-        const T* v = static_cast<const T*>(a.v) + (int64_t)(it.k0 + j) * a.v_stride + kh * d;
-        float s = 0.f, dp = 0.f;
+      for (int e = 0; e < 8; ++e) s = fmaf(to_f32(o.v[e]), to_f32(g.v[e]), s);
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < d) {
-            s = fmaf(fq[i], to_f32(k[lane + 32 * i]), s);
-            dp = fmaf(fd[i], to_f32(v[lane + 32 * i]), dp);
-          }
-        s = warp_sum(s);
-        dp = warp_sum(dp);
-        const float ds = __expf(s - lse) * (dp - dl) * a.scale;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < d) dq[i] = fmaf(ds, to_f32(k[lane + 32 * i]), dq[i]);
-      }
-      T* o = static_cast<T*>(a.dq) + row * a.dq_stride + head * d;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < d) o[lane + 32 * i] = from_f32<T>(dq[i]);
+    for (int m = 8; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (i < n && sub == 0) {
+      const float lse = a.lse[i];
+      rows[i] = RowValue{lse == -INFINITY ? INFINITY : lse * kLog2e, s};
     }
   }
 }
 
-// dk and dv: a warp per key row, over the tokens and query heads that read it.
+struct BwdShared {
+  uint64_t kv_full, kv_empty;                         // the resident pair of tiles
+  uint64_t full[2 * kMaxPairs], empty[2 * kMaxPairs]; // the ring
+  uint64_t row_full[kMaxPairs];
+  uint64_t s_full[2], dp_full, p_full, ds_full, acc_full, drain;
+  uint32_t tmem;
+  int abort;
+  alignas(16) RowValue rows[kMaxPairs][kAttnRows];
+  alignas(16) int last_key[kMaxPairs][kAttnRows];                 // the last local key that the row sees
+};
+
+__device__ __forceinline__ int deal(int round) {
+  return round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+__device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b); }
+
+__device__ __forceinline__ void bwd_init(BwdShared& sh) {
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&sh.kv_full), 1);
+    mbar_init(smem_u32(&sh.kv_empty), 1);
+    for (int i = 0; i < 2 * kMaxPairs; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < kMaxPairs; ++i) mbar_init(smem_u32(&sh.row_full[i]), 1);
+    mbar_init(smem_u32(&sh.s_full[0]), 1);
+    mbar_init(smem_u32(&sh.s_full[1]), 1);
+    mbar_init(smem_u32(&sh.dp_full), 1);
+    mbar_init(smem_u32(&sh.p_full), 8);
+    mbar_init(smem_u32(&sh.ds_full), 8);
+    mbar_init(smem_u32(&sh.acc_full), 1);
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if ((threadIdx.x >> 5) == 9) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+}
+
+__device__ __forceinline__ void bwd_end(BwdShared& sh, uint32_t tmem, int32_t* status) {
+  tc_fence_before();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && sh.abort && status != nullptr) {
+    status[0] = kTimeout;
+    status[1] = -1;
+  }
+}
+
+// After an abort: this thread's last loads (n into the ring, `pairs` into the resident tiles) land on
+// their own; wait for them before the CTA ends.
+__device__ __forceinline__ void drain_loads(BwdShared& sh, uint32_t n, uint32_t stages, uint32_t pairs) {
+  const uint64_t t0 = global_timer_ns();
+  while (pairs > 0 && !mbar_try_wait(smem_u32(&sh.kv_full), (pairs - 1) & 1u) && global_timer_ns() - t0 < kAttnWaitNs) {
+  }
+  for (uint32_t i = n - (n < stages ? n : stages); i < n; ++i)
+    while (!mbar_try_wait(smem_u32(&sh.full[i % stages]), (i / stages) & 1u) && global_timer_ns() - t0 < kAttnWaitNs) {
+    }
+}
+
+// ... and the matrix instructions in flight.
+__device__ __forceinline__ void drain_mma(BwdShared& sh) {
+  if (elect_one()) umma_commit(smem_u32(&sh.drain));
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(smem_u32(&sh.drain), 0) && global_timer_ns() - t0 < kAttnWaitNs) {
+  }
+  __syncwarp();
+}
+
+// One tile's column blocks from a [rows][heads][head_dim] tensor.
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int nb, int head, int row) {
+  for (int b = 0; b < nb; ++b) tma_load_3d(dst + (uint32_t)b * kColBlockBytes, map, bar, b * kColBlock, head, row);
+}
+
+// D = A B^T over the head's columns: both tiles K-major in shared memory.
 template <typename T>
-__global__ void __launch_bounds__(256) attn_dkv_kernel(const AttnArgs a) {
-  const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
-  const AttnKeyItem* items = reinterpret_cast<const AttnKeyItem*>(a.plan + a.l.at_keys);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim;
-  const float* delta = static_cast<const float*>(a.workspace);
-  for (int w = blockIdx.x; w < hdr->n_keys * hk; w += gridDim.x) {
-    const AttnKeyItem it = items[w / hk];
-    const int kh = w % hk;
-    for (int j = warp; j < it.kn; j += 8) {
-      const T* k = static_cast<const T*>(a.k) + (int64_t)(it.k0 + j) * a.k_stride + kh * d;
-      const T* v = static_cast<const T*>(a.v) + (int64_t)(it.k0 + j) * a.v_stride + kh * d;
-      float fk[4], fv[4], dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int ksteps) {
+  const uint64_t ad = sw128_desc(a_tile), bd = sw128_desc(b_tile);
+  for (int k = 0; k < ksteps; ++k) {
+    const uint64_t o = (uint64_t)((k >> 2) * (kColBlockBytes >> 4) + (k & 3) * 2);
+    umma_bf16(d_tmem, ad + o, bd + o, idesc_16<T>(128, 128, false), k > 0);
+  }
+}
+
+// D (+)= A B with A (128 x 128, 16-bit) in tensor memory: the first 64 columns of its contraction
+// packed from column `a_tmem` on, the other 64 from a_tmem + 64 on (each half of the score warps
+// writes over the columns that it read itself).
+__device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_tile, uint32_t id, bool first) {
+  const uint64_t bd = sw128_desc_rows(b_tile);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in = lane + 32 * i < d;
-        fk[i] = in ? to_f32(k[lane + 32 * i]) * a.scale : 0.f;
-        fv[i] = in ? to_f32(v[lane + 32 * i]) : 0.f;
-      }
-      for (int r = max(0, j - it.off) * g; r < it.qn * g; ++r) {
-        const int64_t row = it.q0 + r / g;
-        const int head = kh * g + r % g;
-        const T* q = static_cast<const T*>(a.q) + row * a.q_stride + head * d;
-        const T* dd = static_cast<const T*>(a.dout) + row * a.dout_stride + head * d;
-        float s = 0.f, dp = 0.f, fq[4], fd[4];
+  for (int k = 0; k < 8; ++k)
+    umma_ta(d_tmem, a_tmem + (uint32_t)(k < 4 ? 8 * k : 64 + 8 * (k - 4)), bd + (uint64_t)(128 * k), id, !first || k > 0);
+}
+
+// 16-bit rows of an accumulator, columns [c0, c1) in steps of 16, times `f`.
+template <typename T>
+__device__ __forceinline__ void store_rows(uint32_t acc, int c0, int c1, int d, float f, T* out, bool live, bool have) {
+  for (int c = c0; c < c1; c += 16) {
+    uint32_t o[16] = {};
+    if (have) {
+      tmem_ld_32x32b_x16(acc + (uint32_t)c, o);
+      tmem_wait_ld();
+    }
+    if (!live) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool in = lane + 32 * i < d;
-          fq[i] = in ? to_f32(q[lane + 32 * i]) : 0.f;
-          fd[i] = in ? to_f32(dd[lane + 32 * i]) : 0.f;
-          s = fmaf(fq[i], fk[i], s);
-          dp = fmaf(fd[i], fv[i], dp);
-        }
-        s = warp_sum(s);
-        dp = warp_sum(dp);
-        const float p = __expf(s - a.lse[row * a.s.heads_q + head]);
-        const float ds = p * (dp - delta[row * a.s.heads_q + head]) * a.scale;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dv[i] = fmaf(p, fd[i], dv[i]);
-          dk[i] = fmaf(ds, fq[i], dk[i]);
-        }
-      }
-      T* ok = static_cast<T*>(a.dk) + (int64_t)(it.k0 + j) * a.dk_stride + kh * d;
-      T* ov = static_cast<T*>(a.dv) + (int64_t)(it.k0 + j) * a.dv_stride + kh * d;
+    for (int e = 0; e < 16; e += 8) {
+      uint32_t v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < d) {
-          ok[lane + 32 * i] = from_f32<T>(dk[i]);
-          ov[lane + 32 * i] = from_f32<T>(dv[i]);
-        }
+        v[i] = pack2<T>(__uint_as_float(o[e + 2 * i]) * f, __uint_as_float(o[e + 2 * i + 1]) * f);
+      if (c + e < d) *reinterpret_cast<uint4*>(out + c + e) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
+}
+
+// Query tiles [first token, tiles) that see any key of a key item.
+struct TileRange {
+  int t0, n;
+};
+__device__ __forceinline__ TileRange query_tiles(const AttnKeyItem& it, int tok) {
+  const int from = max(0, -it.off);
+  if (from >= it.qn) return TileRange{0, 0};
+  const int t0 = from / tok * tok;
+  return TileRange{t0, ceil_div(it.qn - t0, tok)};
+}
+
+// ---------------------------------------------------------------------------
+// dk, dv.  Resident: the tiles of K and V.  Ring: pairs (Q, dO).  Scores are transposed (lane = key),
+// so that P^T and dS^T are A operands in tensor memory and Q and dO are read with their rows as the
+// contraction.  Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK: 128 columns each.
+// The tensor core runs dV += P^T dO and the next S^T while the warps make dS^T, and dK += dS^T Q and
+// the next dP^T while they make the next P^T.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_keys_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int pairs) {
+  extern __shared__ uint8_t raw[];
+  __shared__ BwdShared sh;
+  const uint32_t tiles = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim, tok = a.l.tok;
+  const int nb = (d + kColBlock - 1) / kColBlock;
+  const uint32_t tile_bytes = (uint32_t)nb * kColBlockBytes;
+  const uint32_t ring = tiles + 2 * tile_bytes;
+  volatile int* abort_flag = &sh.abort;
+  bwd_init(sh);
+  // ring rows that no load writes (a group that does not divide 128)
+  if (tok * g < kAttnRows && warp < 2 * pairs) zero_tile_rows(ring + (uint32_t)warp * tile_bytes, nb, tok * g);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t st_col = tmem, dpt_col = tmem + 128u, dv_col = tmem + 256u, dk_col = tmem + 384u;
+  const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
+  const AttnKeyItem* items = reinterpret_cast<const AttnKeyItem*>(a.plan + a.l.at_keys);
+  const int works = hdr->n_keys * hk;
+  bool ok = true;
+
+  if (warp < 8) {
+    const int half = warp >> 2;
+    const int key = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t c0 = lanes + 64u * half;
+    const float scale2 = a.scale * kLog2e;
+    uint32_t i = 0, acc = 0;                         // tiles so far (phases and stages), finished items
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnKeyItem it = items[w / hk];
+      const int kh = w % hk;
+      const TileRange tr = query_tiles(it, tok);
+      for (int q = 0; q < tr.n; ++q, ++i) {
+        const uint32_t stg = i % (uint32_t)pairs;
+        if (!mbar_wait_warp<false>(smem_u32(&sh.row_full[stg]), (i / (uint32_t)pairs) & 1u, abort_flag, kAttnWaitNs) ||
+            !mbar_wait_warp<false>(smem_u32(&sh.s_full[0]), i & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[64];
+        tmem_ld_32x32b_x32(st_col + c0, *reinterpret_cast<uint32_t(*)[32]>(s));
+        tmem_ld_32x32b_x32(st_col + c0 + 32u, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+        tmem_wait_ld();
+        const int t = tr.t0 + q * tok;
+        // every row of the tile is there and sees every key
+        const bool whole = t + tok <= it.qn && it.off >= it.kn - 1 - t;
+        const RowValue* rv = sh.rows[stg] + 64 * half;
+        const int* lk = sh.last_key[stg] + 64 * half;
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          const float x = fmaf(__uint_as_float(s[e]), scale2, -rv[e].lse2);
+          s[e] = __float_as_uint(exp2_approx(x));
+        }
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (key > lk[e]) s[e] = 0;
+        }
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) pk[e >> 1] = pack2<T>(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        tmem_st_32x32b_x32(st_col + c0, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full));
+        if (!mbar_wait_warp<false>(smem_u32(&sh.dp_full), i & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t dp[32];
+          tmem_ld_32x32b_x32(dpt_col + c0 + 32u * c, dp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float ds = __uint_as_float(s[32 * c + e]) * (__uint_as_float(dp[e]) - rv[32 * c + e].delta);
+            dp[e] = !whole && key > lk[32 * c + e] ? 0u : __float_as_uint(ds);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) pk[16 * c + (e >> 1)] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+        }
+        tmem_st_32x32b_x32(dpt_col + c0, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ds_full));
+      }
+      if (!ok) break;
+      if (tr.n > 0) {
+        if (!mbar_wait_warp<false>(smem_u32(&sh.acc_full), acc & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        ++acc;
+        tc_fence_after();
+      }
+      const int64_t krow = (int64_t)it.k0 + key;
+      T* out = half == 0 ? static_cast<T*>(a.dv) + krow * a.dv_stride : static_cast<T*>(a.dk) + krow * a.dk_stride;
+      store_rows<T>((half == 0 ? dv_col : dk_col) + lanes, 0, d, d, half == 0 ? 1.f : a.scale, out + kh * d, key < it.kn,
+                    tr.n > 0);
+      tc_fence_before();
+    }
+  } else if (warp == 8) {
+    if (lane == 0) {
+      uint32_t n = 0, np = 0;
+      const uint32_t stages = 2u * (uint32_t)pairs, q_bytes = (uint32_t)(nb * tok * g) * 128u;
+      auto load = [&](const CUtensorMap* map, int head, int row) {
+        const uint32_t st = n % stages;
+        if (!mbar_wait(smem_u32(&sh.empty[st]), ((n / stages) & 1u) ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        mbar_arrive_expect_tx(smem_u32(&sh.full[st]), q_bytes);
+        load_tile(ring + st * tile_bytes, map, smem_u32(&sh.full[st]), nb, head, row);
+        ++n;
+        return true;
+      };
+      for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+        const AttnKeyItem it = items[w / hk];
+        const int kh = w % hk;
+        const TileRange tr = query_tiles(it, tok);
+        if (tr.n == 0) continue;
+        if (!mbar_wait(smem_u32(&sh.kv_empty), (np & 1u) ^ 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(smem_u32(&sh.kv_full), 2 * tile_bytes);
+        load_tile(tiles, &map_k, smem_u32(&sh.kv_full), nb, kh, it.k0);
+        load_tile(tiles + tile_bytes, &map_v, smem_u32(&sh.kv_full), nb, kh, it.k0);
+        ++np;
+        for (int q = 0; ok && q < tr.n; ++q) {
+          ok = load(&map_q, kh * g, it.q0 + tr.t0 + q * tok);
+          if (ok) ok = load(&map_do, kh * g, it.q0 + tr.t0 + q * tok);
+        }
+      }
+      if (*abort_flag) drain_loads(sh, n, stages, np);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    const uint32_t id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
+    const int ksteps = (d + 15) / 16;
+    const uint32_t stages = 2u * (uint32_t)pairs;
+    uint32_t i = 0, np = 0;
+    auto tile = [&](uint32_t n) { return ring + (n % stages) * tile_bytes; };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(smem_u32(bar));
+      __syncwarp();
+    };
+    // the n-th ring tile has landed; rows past the sequence's end are zeroed (they belong to others,
+    // and 0 * NaN is NaN)
+    auto wait_tile = [&](uint32_t n, int have) {
+      if (!mbar_wait_warp<false>(smem_u32(&sh.full[n % stages]), (n / stages) & 1u, abort_flag, kAttnWaitNs)) return false;
+      if (have < tok) zero_tile_rows(tile(n), nb, have * g);
+      return true;
+    };
+    auto scores = [&](uint32_t n, uint32_t resident, uint32_t d_col, uint64_t* bar) {
+      if (elect_one()) {
+        mma_scores<T>(d_col, resident, tile(n), ksteps);
+        umma_commit(smem_u32(bar));
+      }
+      __syncwarp();
+    };
+    auto sum = [&](uint32_t d_col, uint32_t a_col, uint32_t n, bool first) {
+      if (elect_one()) mma_sum(d_col, a_col, tile(n), id_acc, first);
+      __syncwarp();
+    };
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnKeyItem it = items[w / hk];
+      const TileRange tr = query_tiles(it, tok);
+      if (tr.n == 0) continue;
+      auto have = [&](int q) { return it.qn - (tr.t0 + q * tok); };
+      ok = mbar_wait_warp<false>(smem_u32(&sh.kv_full), np & 1u, abort_flag, kAttnWaitNs);
+      ++np;
+      if (ok) ok = wait_tile(2 * i, have(0));
+      if (ok) scores(2 * i, tiles, st_col, &sh.s_full[0]);
+      if (ok) ok = wait_tile(2 * i + 1, have(0));
+      if (ok) scores(2 * i + 1, tiles + tile_bytes, dpt_col, &sh.dp_full);
+      for (int q = 0; ok && q < tr.n; ++q, ++i) {
+        const bool more = q + 1 < tr.n;
+        if (!mbar_wait_warp<false>(smem_u32(&sh.p_full), i & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        sum(dv_col, st_col, 2 * i + 1, q == 0);                     // dV += P^T dO
+        if (more) {
+          if (!wait_tile(2 * i + 2, have(q + 1))) {
+            ok = false;
+            break;
+          }
+          scores(2 * i + 2, tiles, st_col, &sh.s_full[0]);
+        }
+        if (!mbar_wait_warp<false>(smem_u32(&sh.ds_full), i & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        sum(dk_col, dpt_col, 2 * i, q == 0);                        // dK += dS^T Q
+        commit(&sh.empty[(2 * i) % stages]);
+        commit(&sh.empty[(2 * i + 1) % stages]);
+        if (more) {
+          if (!wait_tile(2 * i + 3, have(q + 1))) {
+            ok = false;
+            break;
+          }
+          scores(2 * i + 3, tiles + tile_bytes, dpt_col, &sh.dp_full);
+        } else {
+          commit(&sh.acc_full);
+          commit(&sh.kv_empty);
+        }
+      }
+    }
+    if (!ok) drain_mma(sh);
+  } else if (warp == 10) {
+    // each query tile's row values beside it
+    const RowValue* rows = static_cast<const RowValue*>(a.workspace);
+    const uint32_t stages = 2u * (uint32_t)pairs;
+    uint32_t i = 0;
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnKeyItem it = items[w / hk];
+      const int kh = w % hk;
+      const TileRange tr = query_tiles(it, tok);
+      for (int q = 0; q < tr.n; ++q, ++i) {
+        const uint32_t stg = i % (uint32_t)pairs;
+        // free when the matrix instructions on the same pair are done
+        if (!mbar_wait_warp<false>(smem_u32(&sh.empty[(2 * i + 1) % stages]), ((i / (uint32_t)pairs) & 1u) ^ 1u, abort_flag,
+                                   kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        const int t = tr.t0 + q * tok;
+#pragma unroll
+        for (int c = 0; c < kAttnRows; c += 32) {
+          const int x = c + lane, tt = t + x / g;
+          RowValue v{INFINITY, 0.f};
+          int last = -1;
+          if (x < tok * g && tt < it.qn) {
+            v = rows[((int64_t)it.q0 + tt) * a.s.heads_q + kh * g + x % g];
+            last = tt + it.off;
+          }
+          sh.rows[stg][x] = v;
+          sh.last_key[stg][x] = last;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.row_full[stg]));
+      }
+      if (!ok) break;
+    }
+  }
+  bwd_end(sh, tmem, a.status);
+}
+
+// ---------------------------------------------------------------------------
+// dq.  Resident: the tiles of Q and dO.  Ring: K and V blocks, alternating.  Lane = query row; the two
+// halves of the score warps take 64 keys each.  Tensor memory: S (two buffers; dS over the one it
+// came from), dP, dQ.
+// ---------------------------------------------------------------------------
+// Key blocks that tile t of an item reads, over the item's whole range (of a cut item the first
+// piece takes all of it: enough rows to fill the GPU are the rule in training).
+__device__ __forceinline__ int key_blocks(const AttnItem& it, int t, int tok, bool causal) {
+  const int have = min(tok, it.qn - t * tok);
+  if (have <= 0 || it.kb > 0) return 0;
+  const int last = causal ? min(it.kn, max(0, it.off + t * tok + have)) : it.kn;
+  return ceil_div(last, kAttnKeys);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_queries_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int pairs) {
+  extern __shared__ uint8_t raw[];
+  __shared__ BwdShared sh;
+  const uint32_t tiles = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim, tok = a.l.tok;
+  const bool causal = a.s.causal != 0;
+  const int nb = (d + kColBlock - 1) / kColBlock;
+  const uint32_t tile_bytes = (uint32_t)nb * kColBlockBytes;
+  const uint32_t ring = tiles + 2 * tile_bytes;
+  const uint32_t stages = 2u * (uint32_t)pairs;
+  volatile int* abort_flag = &sh.abort;
+  bwd_init(sh);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t dp_col = tmem + 256u, dq_col = tmem + 384u;    // S buffers: tmem, tmem + 128
+  const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
+  const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
+  const int works = hdr->n_items * hk * 2;                      // (item, key head, tile)
+  bool ok = true;
+
+  if (warp < 8) {
+    const int half = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const float scale2 = a.scale * kLog2e;
+    const RowValue* rows = static_cast<const RowValue*>(a.workspace);
+    uint32_t i = 0, acc = 0;
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnItem it = items[w / (2 * hk)];
+      const int t = w & 1, kh = (w >> 1) % hk;
+      if (it.kb > 0 || it.qn <= t * tok) continue;
+      const int n = key_blocks(it, t, tok, causal);
+      const int my_tok = t * tok + row / g, head = kh * g + row % g;
+      const bool live = row < tok * g && my_tok < it.qn;
+      int lim = causal ? min(it.kn, it.off + my_tok + 1) : it.kn;
+      RowValue v{INFINITY, 0.f};
+      if (live) v = rows[((int64_t)it.q0 + my_tok) * a.s.heads_q + head];
+      else lim = 0;
+      for (int j = 0; j < n; ++j, ++i) {
+        const uint32_t s_col = tmem + lanes + (i & 1u) * 128u + 64u * half;
+        if (!mbar_wait_warp<false>(smem_u32(&sh.s_full[i & 1u]), (i >> 1) & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t s[64];
+        tmem_ld_32x32b_x32(s_col, *reinterpret_cast<uint32_t(*)[32]>(s));
+        tmem_ld_32x32b_x32(s_col + 32u, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+        tmem_wait_ld();
+        const int left = lim - j * kAttnKeys - 64 * half;
+        const bool whole = __all_sync(0xffffffffu, left >= 64);
+#pragma unroll
+        for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(s[e]), scale2, -v.lse2)));
+        if (!mbar_wait_warp<false>(smem_u32(&sh.dp_full), i & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t dp[32];
+          tmem_ld_32x32b_x32(dp_col + lanes + 64u * half + 32u * c, dp);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float ds = __uint_as_float(s[32 * c + e]) * (__uint_as_float(dp[e]) - v.delta);
+            dp[e] = !whole && 32 * c + e >= left ? 0u : __float_as_uint(ds);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) pk[16 * c + (e >> 1)] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+        }
+        tmem_st_32x32b_x32(s_col, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ds_full));
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!mbar_wait_warp<false>(smem_u32(&sh.acc_full), acc & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        ++acc;
+        tc_fence_after();
+      }
+      // each half of the warps stores half of the columns
+      const int mid = (d / 2 + 15) / 16 * 16;
+      T* out = static_cast<T*>(a.dq) + ((int64_t)it.q0 + my_tok) * a.dq_stride + head * d;
+      store_rows<T>(dq_col + lanes, half == 0 ? 0 : mid, half == 0 ? mid : d, d, a.scale, out, live, n > 0);
+      tc_fence_before();
+    }
+  } else if (warp == 8) {
+    if (lane == 0) {
+      uint32_t n = 0, np = 0;
+      const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
+      auto load = [&](const CUtensorMap* map, int head, int rowk) {
+        const uint32_t st = n % stages;
+        if (!mbar_wait(smem_u32(&sh.empty[st]), ((n / stages) & 1u) ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        mbar_arrive_expect_tx(smem_u32(&sh.full[st]), tile_bytes);
+        load_tile(ring + st * tile_bytes, map, smem_u32(&sh.full[st]), nb, head, rowk);
+        ++n;
+        return true;
+      };
+      for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+        const AttnItem it = items[w / (2 * hk)];
+        const int t = w & 1, kh = (w >> 1) % hk;
+        const int nk = key_blocks(it, t, tok, causal);
+        if (nk == 0) continue;
+        if (!mbar_wait(smem_u32(&sh.kv_empty), (np & 1u) ^ 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(smem_u32(&sh.kv_full), 2 * q_bytes);
+        load_tile(tiles, &map_q, smem_u32(&sh.kv_full), nb, kh * g, it.q0 + t * tok);
+        load_tile(tiles + tile_bytes, &map_do, smem_u32(&sh.kv_full), nb, kh * g, it.q0 + t * tok);
+        ++np;
+        for (int j = 0; ok && j < nk; ++j) {
+          ok = load(&map_k, kh, it.k0 + j * kAttnKeys);
+          if (ok) ok = load(&map_v, kh, it.k0 + j * kAttnKeys);
+        }
+      }
+      if (*abort_flag) drain_loads(sh, n, stages, np);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    const uint32_t id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
+    const int ksteps = (d + 15) / 16;
+    uint32_t i = 0, np = 0;
+    auto tile = [&](uint32_t n) { return ring + (n % stages) * tile_bytes; };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(smem_u32(bar));
+      __syncwarp();
+    };
+    auto wait_tile = [&](uint32_t n) {
+      return mbar_wait_warp<false>(smem_u32(&sh.full[n % stages]), (n / stages) & 1u, abort_flag, kAttnWaitNs);
+    };
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnItem it = items[w / (2 * hk)];
+      const int n = key_blocks(it, w & 1, tok, causal);
+      if (n == 0) continue;
+      // S(j), into buffer (i + j) & 1; K rows past the sequence's end are zeroed for dQ += dS K
+      auto s_of = [&](int j, uint32_t ii) {
+        if (!wait_tile(2 * ii)) return false;
+        const int have = it.kn - j * kAttnKeys;
+        if (have < kAttnKeys) zero_tile_rows(tile(2 * ii), nb, have);
+        if (elect_one()) {
+          mma_scores<T>(tmem + (ii & 1u) * 128u, tiles, tile(2 * ii), ksteps);
+          umma_commit(smem_u32(&sh.s_full[ii & 1u]));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto dp_of = [&](uint32_t ii) {
+        if (!wait_tile(2 * ii + 1)) return false;
+        if (elect_one()) {
+          mma_scores<T>(dp_col, tiles + tile_bytes, tile(2 * ii + 1), ksteps);
+          umma_commit(smem_u32(&sh.dp_full));
+          umma_commit(smem_u32(&sh.empty[(2 * ii + 1) % stages]));
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = mbar_wait_warp<false>(smem_u32(&sh.kv_full), np & 1u, abort_flag, kAttnWaitNs);
+      ++np;
+      if (ok) ok = s_of(0, i) && dp_of(i);
+      for (int j = 0; ok && j < n; ++j, ++i) {
+        if (j + 1 < n && !s_of(j + 1, i + 1)) {
+          ok = false;
+          break;
+        }
+        if (!mbar_wait_warp<false>(smem_u32(&sh.ds_full), i & 1u, abort_flag, kAttnWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (j + 1 < n && !dp_of(i + 1)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          mma_sum(dq_col, tmem + (i & 1u) * 128u, tile(2 * i), id_acc, j == 0);
+          umma_commit(smem_u32(&sh.empty[(2 * i) % stages]));
+        }
+        __syncwarp();
+        if (j + 1 == n) {
+          commit(&sh.acc_full);
+          commit(&sh.kv_empty);
+        }
+      }
+    }
+    if (!ok) drain_mma(sh);
+  }
+  bwd_end(sh, tmem, a.status);
 }
 
 template <typename T>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
-  const int64_t wq = a.l.cap_items * a.s.heads_kv, wk = a.l.cap_keys * a.s.heads_kv;
-  if (wq > 0) attn_dq_kernel<T><<<(unsigned)(wq < 1216 ? wq : 1216), 256, 0, st>>>(a);
-  if (wk > 0) attn_dkv_kernel<T><<<(unsigned)(wk < 1216 ? wk : 1216), 256, 0, st>>>(a);
+  const vitfe_attention_shape& s = a.s;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (s.rows_q * s.heads_q + 15) / 16;
+  attn_rows_kernel<T><<<(unsigned)(blocks < 1 ? 1 : blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(a);
+  const int tile = (s.head_dim + kColBlock - 1) / kColBlock * kColBlockBytes;
+  int pairs = (kSmemMax - 1024 - (int)sizeof(BwdShared) - 2 * tile) / (2 * tile);
+  if (pairs > kMaxPairs) pairs = kMaxPairs;
+  const int smem = (2 + 2 * pairs) * tile + 1024;
+  CUtensorMap mq, md, mk, mv;
+  if (s.rows_q > 0 && s.rows_k > 0) {
+    if (!make_head_map(&mq, a.q, s.dtype, s.head_dim, s.heads_q, s.rows_q, a.q_stride, a.l.group, a.l.tok) ||
+        !make_head_map(&md, a.dout, s.dtype, s.head_dim, s.heads_q, s.rows_q, a.dout_stride, a.l.group, a.l.tok) ||
+        !make_head_map(&mk, a.k, s.dtype, s.head_dim, s.heads_kv, s.rows_k, a.k_stride, 1, kAttnKeys) ||
+        !make_head_map(&mv, a.v, s.dtype, s.head_dim, s.heads_kv, s.rows_k, a.v_stride, 1, kAttnKeys))
+      return cudaErrorInvalidValue;
+  } else if (s.rows_q > 0 || s.rows_k > 0) {
+    // one side is empty: every item stores zeros and nothing is loaded, so any valid map will do
+    const void* p = s.rows_q > 0 ? a.q : a.k;
+    const int64_t rows = s.rows_q > 0 ? s.rows_q : s.rows_k, stride = s.rows_q > 0 ? a.q_stride : a.k_stride;
+    if (!make_head_map(&mq, p, s.dtype, s.head_dim, 1, rows, stride, 1, kAttnKeys)) return cudaErrorInvalidValue;
+    md = mk = mv = mq;
+  }
+  const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * 2;
+  if (s.rows_k > 0) {
+    e = cudaFuncSetAttribute(attn_keys_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attn_keys_kernel<T><<<(unsigned)(wk < sms ? wk : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, pairs);
+  }
+  if (s.rows_q > 0) {
+    e = cudaFuncSetAttribute(attn_queries_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attn_queries_kernel<T><<<(unsigned)(wq < sms ? wq : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, pairs);
+  }
   return cudaGetLastError();
 }
 
