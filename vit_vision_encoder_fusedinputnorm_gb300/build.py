@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvitfe.so")
 SOURCES = ["vitfe_host.cu", "vitfe_embed.cu", "vitfe_aux.cu", "vitfe_block_host.cu", "vitfe_norm.cu",
-           "vitfe_mrope.cu", "vitfe_attn.cu", "vitfe_attn_bwd.cu"]
+           "vitfe_norm_bwd.cu", "vitfe_mrope.cu", "vitfe_attn.cu", "vitfe_attn_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -665,11 +665,11 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   int stages = (kSmemMax - 2048 - 2 * tile) / tile;      // 2 KB: alignment and the barriers
   if (stages > kMaxStages) stages = kMaxStages;
   const int smem = (2 + stages) * tile + 1024;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<uint64_t> allowed{0};
+  int sms = 0;
+  cudaError_t e = current_sms(&sms);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = allow_smem(reinterpret_cast<const void*>(attn_kernel<T>), kSmemMax - (int)sizeof(FwdShared), allowed);
   if (e != cudaSuccess) return e;
   const int64_t work = a.l.cap_items * s.heads_kv;
   attn_kernel<T><<<(unsigned)(work < sms ? work : sms), kFwdThreads, smem, st>>>(a, mq, mk, mv, stages);

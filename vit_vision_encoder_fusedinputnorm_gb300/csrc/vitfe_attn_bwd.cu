@@ -665,9 +665,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 template <typename T>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   const vitfe_attention_shape& s = a.s;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<uint64_t> allowed_keys{0}, allowed_queries{0};
+  int sms = 0;
+  cudaError_t e = current_sms(&sms);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (s.rows_q * s.heads_q + 15) / 16;
   attn_rows_kernel<T><<<(unsigned)(blocks < 1 ? 1 : blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(a);
@@ -691,12 +691,13 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   }
   const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * 2;
   if (s.rows_k > 0) {
-    e = cudaFuncSetAttribute(attn_keys_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = allow_smem(reinterpret_cast<const void*>(attn_keys_kernel<T>), kSmemMax - (int)sizeof(BwdShared), allowed_keys);
     if (e != cudaSuccess) return e;
     attn_keys_kernel<T><<<(unsigned)(wk < sms ? wk : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, pairs);
   }
   if (s.rows_q > 0) {
-    e = cudaFuncSetAttribute(attn_queries_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = allow_smem(reinterpret_cast<const void*>(attn_queries_kernel<T>), kSmemMax - (int)sizeof(BwdShared),
+                   allowed_queries);
     if (e != cudaSuccess) return e;
     attn_queries_kernel<T><<<(unsigned)(wq < sms ? wq : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, pairs);
   }

@@ -1,6 +1,8 @@
 // Definitions shared by the encoder-block operators (layer norm, multi-axis rotary, attention).
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "vitfe_internal.cuh"
@@ -49,34 +51,39 @@ struct alignas(sizeof(T) * V) Vec {
   T v[V];
 };
 
-// V parameters of any type as floats (the pointer aligned to 16 bytes when V > 1).
-template <int V>
-__device__ __forceinline__ void load_params(const void* p, vitfe_dtype d, int c, float (&out)[V]) {
-  if (d == VITFE_F32) {
-    constexpr int W = V < 4 ? V : 4;
-#pragma unroll
-    for (int i = 0; i < V; i += W) {
-      const Vec<float, W> x = *reinterpret_cast<const Vec<float, W>*>(static_cast<const float*>(p) + c + i);
-#pragma unroll
-      for (int e = 0; e < W; ++e) out[i + e] = x.v[e];
-    }
-  } else if (d == VITFE_BF16) {
-    const Vec<__nv_bfloat16, V> x =
-        *reinterpret_cast<const Vec<__nv_bfloat16, V>*>(static_cast<const __nv_bfloat16*>(p) + c);
-#pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = to_f32(x.v[e]);
-  } else {
-    const Vec<__half, V> x = *reinterpret_cast<const Vec<__half, V>*>(static_cast<const __half*>(p) + c);
-#pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = to_f32(x.v[e]);
-  }
+// Two fp32 lanes in one 64-bit register.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
 }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo_f32(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_f32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
+
+// SMs of the current device, asked for once per device.
+cudaError_t current_sms(int* sms);
+// Allow `kernel` up to `smem` bytes of dynamic shared memory on the current device, once per device
+// (`done`: a bit for each device below 64, of this kernel alone).
+cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done);
 
 // ---------------------------------------------------------------------------
 // launchers

@@ -15,8 +15,8 @@ any other call.
 """
 from __future__ import annotations
 
-import functools
-from typing import Optional, Sequence, Tuple
+import contextlib
+from typing import Optional, Sequence
 
 import torch
 
@@ -32,96 +32,107 @@ def _dtype(t: torch.Tensor) -> int:
         raise TypeError(f"bfloat16, float16 or float32 tensors are supported, not {t.dtype}") from None
 
 
-def _on(x: torch.Tensor, stream):
-    return stream if stream is not None else torch.cuda.current_stream(x.device)
+def _current(stream):
+    """Make ``stream`` current, so that outputs and workspaces are that stream's memory."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
 
 
-def _stream_call(fn):
-    """Run fn with ``stream`` current, so that outputs and workspaces are that stream's memory."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
-        if stream is None:
-            return fn(*args, **kwargs)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream)
-        with torch.cuda.stream(stream):
-            return fn(*args, stream=stream, **kwargs)
-    return call
+def _launch(name: str, device: int, *args) -> None:
+    """Call an entry point on the current stream of ``device``."""
+    guard = contextlib.nullcontext() if device == torch.cuda.current_device() else torch.cuda.device(device)
+    with guard:
+        code = getattr(B.load(), name)(*args, torch._C._cuda_getCurrentRawStream(device))
+    if code:
+        raise B.VitfeError(name, code)
 
 
-def _need_cuda(*tensors) -> None:
-    first = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("CUDA tensors are needed")
-        if first is None:
-            first = t.device
-        elif t.device != first:
+def _device(x: torch.Tensor, *others) -> int:
+    """The GPU that all of the tensors are on."""
+    i = x.get_device()
+    if i < 0:
+        raise ValueError("CUDA tensors are needed")
+    for t in others:
+        if t is not None and t.get_device() != i:
             raise ValueError("all tensors have to be on one device")
+    return i
 
 
-def _rows(x: torch.Tensor, name: str) -> Tuple[int, int, int]:
-    """(rows, width, row stride) of a [rows][width] tensor whose rows are contiguous."""
+def _ptr(x: Optional[torch.Tensor]) -> Optional[int]:
+    return None if x is None else x.data_ptr()
+
+
+def _rows(x: torch.Tensor, name: str) -> int:
+    """Row stride of a [rows][width] tensor whose rows are contiguous."""
     if x.dim() != 2:
         raise ValueError(f"{name}: a [rows][width] tensor is needed, not {tuple(x.shape)}")
-    if x.shape[0] and x.shape[1] > 1 and x.stride(1) != 1:
+    rows, width = x.shape
+    row, col = x.stride()
+    if col != 1 and rows and width > 1:
         raise ValueError(f"{name}: its rows have to be contiguous")
-    stride = x.stride(0) if x.shape[0] > 1 else x.shape[1]
-    return x.shape[0], x.shape[1], stride
+    return row if rows > 1 else width
 
 
 def _heads(x: torch.Tensor, name: str) -> int:
     """Row stride of a [rows][heads][head_dim] tensor whose rows are contiguous."""
     if x.dim() != 3:
         raise ValueError(f"{name}: a [rows][heads][head_dim] tensor is needed, not {tuple(x.shape)}")
-    if x.shape[0] and ((x.shape[2] > 1 and x.stride(2) != 1) or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+    rows, heads, dim = x.shape
+    row, head, col = x.stride()
+    if rows and ((col != 1 and dim > 1) or (head != dim and heads > 1)):
         raise ValueError(f"{name}: its rows have to be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+    return row if rows > 1 else heads * dim
 
 
 def _like(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
-def _vector(v: Optional[torch.Tensor], width: int, name: str, dtype: Optional[torch.dtype] = None):
-    if v is None:
-        return
-    if v.shape != (width,) or not v.is_contiguous() or (dtype is not None and v.dtype != dtype):
+def _target(x: torch.Tensor, out: Optional[torch.Tensor], name: str) -> torch.Tensor:
+    if out is None:
+        return _like(x)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"{name}: the input's shape and type are needed")
+    return out
+
+
+def _vector(v: Optional[torch.Tensor], width: int, name: str, dtype: Optional[torch.dtype] = None) -> None:
+    if v is not None and (v.dim() != 1 or v.shape[0] != width or not v.is_contiguous()
+                          or (dtype is not None and v.dtype != dtype)):
         raise ValueError(f"{name}: a contiguous [{width}] tensor{f' of {dtype}' if dtype else ''} is needed")
 
 
 # ------------------------------------------------------------------ layer norm
 
-@_stream_call
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stats: bool = False, stream=None):
     """Layer norm over the rows of x [rows][width]; with ``stats``: (y, mean, rstd) for the backward pass."""
-    rows, width, stride = _rows(x, "x")
-    _need_cuda(x, weight, bias, out)
+    if stream is not None:
+        with _current(stream):
+            return layer_norm(x, weight, bias, eps, out, stats)
+    stride = _rows(x, "x")
+    rows, width = x.shape
+    device = _device(x, weight, bias, out)
     _vector(weight, width, "weight")
     _vector(bias, width, "bias", None if weight is None else weight.dtype)
-    if out is None:
-        out = _like(x)
-    elif out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out: x's shape and type are needed")
+    out = _target(x, out, "out")
     mean = rstd = None
     if stats:
         mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
     params = weight if weight is not None else bias
-    with torch.cuda.device(x.device):
-        B.vitfe_layer_norm(x, stride, _dtype(x), rows, width, weight, bias,
-                           B.VITFE_F32 if params is None else _dtype(params), eps, out, _rows(out, "out")[2], mean,
-                           rstd, _on(x, stream))
+    _launch("vitfe_layer_norm", device, x.data_ptr(), stride, _dtype(x), rows, width, _ptr(weight), _ptr(bias),
+            B.VITFE_F32 if params is None else _dtype(params), eps, out.data_ptr(), _rows(out, "out"), _ptr(mean),
+            _ptr(rstd))
     return (out, mean, rstd) if stats else out
 
 
-@_stream_call
 def layer_norm_backward(dout, x, mean, rstd, weight=None, params: bool = True, stream=None):
     """(dx, dweight, dbias) of layer_norm; the last two float32, or None without ``params``."""
-    rows, width, stride = _rows(x, "x")
-    _need_cuda(dout, x, mean, rstd, weight)
+    if stream is not None:
+        with _current(stream):
+            return layer_norm_backward(dout, x, mean, rstd, weight, params)
+    stride = _rows(x, "x")
+    rows, width = x.shape
+    device = _device(x, dout, mean, rstd, weight)
     if dout.shape != x.shape or dout.dtype != x.dtype:
         raise ValueError("dout: x's shape and type are needed")
     _vector(weight, width, "weight")
@@ -132,13 +143,12 @@ def layer_norm_backward(dout, x, mean, rstd, weight=None, params: bool = True, s
     size = 0
     if params:
         dweight = torch.empty(width, dtype=torch.float32, device=x.device)
-        dbias = torch.empty(width, dtype=torch.float32, device=x.device)
+        dbias = torch.empty_like(dweight)
         size = B.vitfe_layer_norm_workspace(rows, width)
         work = torch.empty(size, dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
-        B.vitfe_layer_norm_backward(dout, _rows(dout, "dout")[2], x, stride, _dtype(x), rows, width, weight,
-                                    B.VITFE_F32 if weight is None else _dtype(weight), mean, rstd, dx, width, dweight,
-                                    dbias, work, size, _on(x, stream))
+    _launch("vitfe_layer_norm_backward", device, dout.data_ptr(), _rows(dout, "dout"), x.data_ptr(), stride, _dtype(x),
+            rows, width, _ptr(weight), B.VITFE_F32 if weight is None else _dtype(weight), mean.data_ptr(),
+            rstd.data_ptr(), dx.data_ptr(), width, _ptr(dweight), _ptr(dbias), _ptr(work), size)
     return dx, dweight, dbias
 
 
@@ -156,14 +166,16 @@ def section_axes(sections: Sequence[int], interleaved: bool = False) -> list:
     return [i % n if i % n and i < n * sections[i % n] else 0 for i in range(total)]
 
 
-@_stream_call
 def mrope_positions(spans, n_spans, items, n_items, rows: int, merge: int = 2, pos=None, status=None, stream=None):
     """int32 [3][rows] positions of a packed prompt (vitfe_mrope_positions).
 
     spans: int32 [capacity][4] on the device (first, text, item, step); items: the item table of
     ``FrontEnd.upload`` (24 bytes an item), or None.
     """
-    _need_cuda(spans, n_spans, items, n_items, pos, status)
+    if stream is not None:
+        with _current(stream):
+            return mrope_positions(spans, n_spans, items, n_items, rows, merge, pos, status)
+    device = _device(spans, n_spans, items, n_items, pos, status)
     if spans.dtype != torch.int32 or spans.dim() != 2 or spans.shape[1] != 4 or not spans.is_contiguous():
         raise ValueError("spans: a contiguous int32 [capacity][4] tensor is needed")
     if n_spans.dtype != torch.int32 or (n_items is not None and n_items.dtype != torch.int32):
@@ -177,13 +189,11 @@ def mrope_positions(spans, n_spans, items, n_items, rows: int, merge: int = 2, p
         pos = torch.empty((3, rows), dtype=torch.int32, device=spans.device)
     elif pos.shape != (3, rows) or pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ValueError("pos: a contiguous int32 [3][rows] tensor is needed")
-    with torch.cuda.device(spans.device):
-        B.vitfe_mrope_positions(spans, n_spans, spans.shape[0], items, n_items, capacity, merge, rows, pos, status,
-                                _on(spans, stream))
+    _launch("vitfe_mrope_positions", device, spans.data_ptr(), n_spans.data_ptr(), spans.shape[0], _ptr(items),
+            _ptr(n_items), capacity, merge, rows, pos.data_ptr(), _ptr(status))
     return pos
 
 
-@_stream_call
 def mrope_apply(q, k, pos, axes: Sequence[int], theta: float = 10000.0, inverse: bool = False, q_out=None, k_out=None,
                 stream=None):
     """(q, k) rotated: [rows][heads][head_dim] each, either may be None.
@@ -191,28 +201,31 @@ def mrope_apply(q, k, pos, axes: Sequence[int], theta: float = 10000.0, inverse:
     pos: int32 [n axes][rows]; axes: the axis of each pair (``section_axes``), rotary_dim / 2 of
     them.  q_out, k_out: where to write (q and k themselves for in place), else new tensors.
     """
+    if stream is not None:
+        with _current(stream):
+            return mrope_apply(q, k, pos, axes, theta, inverse, q_out, k_out)
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")
-    _need_cuda(q, k, pos, q_out, k_out)
-    if k is not None and (k.dtype != x.dtype or k.shape[0] != x.shape[0] or k.shape[2] != x.shape[2]):
-        raise ValueError("q and k: the same rows, head_dim and type are needed")
-    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[1] != x.shape[0] or not pos.is_contiguous():
+    device = _device(x, q, k, pos, q_out, k_out)
+    if q is not None:
+        q_out = _target(q, q_out, "q_out")
+        tq = (q.data_ptr(), q.shape[1], _heads(q, "q"), q_out.data_ptr(), _heads(q_out, "q_out"))
+    else:
+        tq = (None, 0, 0, None, 0)
+    if k is not None:
+        if k.dtype != x.dtype or k.shape[0] != x.shape[0] or k.shape[2] != x.shape[2]:
+            raise ValueError("q and k: the same rows, head_dim and type are needed")
+        k_out = _target(k, k_out, "k_out")
+        tk = (k.data_ptr(), k.shape[1], _heads(k, "k"), k_out.data_ptr(), _heads(k_out, "k_out"))
+    else:
+        tk = (None, 0, 0, None, 0)
+    rows, _, dim = x.shape
+    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[1] != rows or not pos.is_contiguous():
         raise ValueError("pos: a contiguous int32 [axes][rows] tensor is needed")
-
-    def target(x, out, name):
-        if x is None:
-            return None, 0, 0, None, 0
-        out = _like(x) if out is None else out
-        if out.shape != x.shape or out.dtype != x.dtype:
-            raise ValueError(f"{name}: the input's shape and type are needed")
-        return x, x.shape[1], _heads(x, name), out, _heads(out, name)
-
-    tq, tk = target(q, q_out, "q_out"), target(k, k_out, "k_out")
-    with torch.cuda.device(x.device):
-        B.vitfe_mrope_apply(pos, pos.shape[0], bytes(axes), 2 * len(axes), theta, inverse, x.shape[0], x.shape[2],
-                            _dtype(x), *tq, *tk, _on(x, stream))
-    return tq[3], tk[3]
+    _launch("vitfe_mrope_apply", device, pos.data_ptr(), pos.shape[0], bytes(axes), 2 * len(axes), theta, bool(inverse),
+            rows, dim, _dtype(x), *tq, *tk)
+    return q_out, k_out
 
 
 # ------------------------------------------------------------------ attention
@@ -224,82 +237,84 @@ class AttentionPlan:
     queries and keys share one).  rows_q, rows_k: rows of q and of k, v, padding included.
     """
 
-    @_stream_call
     def __init__(self, cu_q, cu_k, rows_q: int, rows_k: int, heads_q: int, heads_kv: int, head_dim: int,
                  causal: bool = False, status=None, stream=None):
-        _need_cuda(cu_q, cu_k, status)
-        for c in (cu_q, cu_k):
-            if c.dtype != torch.int32 or c.dim() != 1 or not c.is_contiguous() or c.shape != cu_q.shape or not len(c):
-                raise ValueError("cu_q, cu_k: contiguous int32 [sequences + 1] tensors of one length are needed")
-        self.shape = B.AttentionShape(rows_q, rows_k, len(cu_q) - 1, heads_q, heads_kv, head_dim, int(causal),
-                                      B.VITFE_BF16)
-        self.device = cu_q.device
-        size = B.vitfe_attention_plan_bytes(self.shape)
-        self.buffer = torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
-        self.update(cu_q, cu_k, status, stream=stream)
+        self.device = _device(cu_q, cu_k, status)
+        if cu_q.dim() != 1 or not len(cu_q):
+            raise ValueError("cu_q: an int32 [sequences + 1] tensor is needed")
+        shape = (rows_q, rows_k, len(cu_q) - 1, heads_q, heads_kv, head_dim, int(causal))
+        # one shape for each type that a call may have: workspaces do not depend on it
+        self._shapes = {t: B.AttentionShape(*shape, _DTYPES[t]) for t in (torch.bfloat16, torch.float16)}
+        self.shape = self._shapes[torch.bfloat16]
+        self._q, self._k = (rows_q, heads_q, head_dim), (rows_k, heads_kv, head_dim)
+        self._work = B.vitfe_attention_workspace(self.shape)
+        self._work_backward = B.vitfe_attention_backward_workspace(self.shape)
+        with contextlib.nullcontext() if stream is None else _current(stream):
+            size = B.vitfe_attention_plan_bytes(self.shape)
+            self.buffer = torch.empty(max(size, 16), dtype=torch.uint8, device=cu_q.device)
+            self.update(cu_q, cu_k, status)
 
-    @_stream_call
     def update(self, cu_q, cu_k, status=None, stream=None) -> None:
         """Plan new boundaries in the same buffer (the shape stays: a captured graph replays this)."""
-        with torch.cuda.device(self.device):
-            B.vitfe_attention_plan(self.shape, cu_q, cu_k, self.buffer, status, _on(cu_q, stream))
+        if stream is not None:
+            with _current(stream):
+                return self.update(cu_q, cu_k, status)
+        device = _device(self.buffer, cu_q, cu_k, status)
+        for c in (cu_q, cu_k):
+            if c.dtype != torch.int32 or not c.is_contiguous() or c.shape != (self.shape.max_seqs + 1,):
+                raise ValueError(f"cu_q, cu_k: contiguous int32 [{self.shape.max_seqs + 1}] tensors are needed")
+        _launch("vitfe_attention_plan", device, self.shape, cu_q.data_ptr(), cu_k.data_ptr(), self.buffer.data_ptr(),
+                _ptr(status))
 
     def of(self, q, k, v) -> "B.AttentionShape":
         """The shape of a call with these tensors; raises where they do not fit the plan."""
-        s = self.shape
-        if q.dim() != 3 or q.shape != (s.rows_q, s.heads_q, s.head_dim):
-            raise ValueError(f"q: {(s.rows_q, s.heads_q, s.head_dim)} is planned, not {tuple(q.shape)}")
-        for t, name in ((k, "k"), (v, "v")):
-            if t.dim() != 3 or t.shape != (s.rows_k, s.heads_kv, s.head_dim):
-                raise ValueError(f"{name}: {(s.rows_k, s.heads_kv, s.head_dim)} is planned, not {tuple(t.shape)}")
-            if t.dtype != q.dtype:
-                raise ValueError("q, k, v: one type is needed")
-        if q.device != self.device:
-            raise ValueError("the plan is on another device")
-        return B.AttentionShape(s.rows_q, s.rows_k, s.max_seqs, s.heads_q, s.heads_kv, s.head_dim, s.causal, _dtype(q))
+        if q.shape != self._q:
+            raise ValueError(f"q: {self._q} is planned, not {tuple(q.shape)}")
+        if k.shape != self._k or v.shape != self._k:
+            raise ValueError(f"k, v: {self._k} is planned, not {tuple(k.shape)}, {tuple(v.shape)}")
+        dtype = q.dtype
+        if k.dtype != dtype or v.dtype != dtype or dtype not in self._shapes:
+            raise ValueError("q, k, v: one type, bfloat16 or float16, is needed")
+        return self._shapes[dtype]
 
 
-def _work(size: int, device):
-    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
-
-
-@_stream_call
 def attention(q, k, v, plan: AttentionPlan, scale: Optional[float] = None, lse: bool = False, out=None, status=None,
               stream=None):
     """softmax(scale q k^T) v over the plan's sequences; with ``lse``: (out, lse float32 [rows][heads])."""
-    _need_cuda(q, k, v, out, status)
+    if stream is not None:
+        with _current(stream):
+            return attention(q, k, v, plan, scale, lse, out, status)
     shape = plan.of(q, k, v)
-    if out is None:
-        out = _like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out: q's shape and type are needed")
-    sums = torch.empty((shape.rows_q, shape.heads_q), dtype=torch.float32, device=q.device) if lse else None
-    with torch.cuda.device(q.device):
-        B.vitfe_attention(shape, plan.buffer, q, _heads(q, "q"), k, _heads(k, "k"), v, _heads(v, "v"),
-                          shape.head_dim ** -0.5 if scale is None else scale, out, _heads(out, "out"), sums,
-                          _work(B.vitfe_attention_workspace(shape), q.device), status, _on(q, stream))
+    device = _device(plan.buffer, q, k, v, out, status)
+    out = _target(q, out, "out")
+    sums = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse else None
+    work = torch.empty(plan._work, dtype=torch.uint8, device=q.device) if plan._work else None
+    _launch("vitfe_attention", device, shape, plan.buffer.data_ptr(), q.data_ptr(), _heads(q, "q"), k.data_ptr(),
+            _heads(k, "k"), v.data_ptr(), _heads(v, "v"), q.shape[2] ** -0.5 if scale is None else scale,
+            out.data_ptr(), _heads(out, "out"), _ptr(sums), _ptr(work), _ptr(status))
     return (out, sums) if lse else out
 
 
-@_stream_call
 def attention_backward(dout, q, k, v, out, lse, plan: AttentionPlan, scale: Optional[float] = None, status=None,
                        stream=None):
     """(dq, dk, dv) of attention; ``out`` and ``lse`` are the forward pass's."""
-    _need_cuda(dout, q, k, v, out, lse, status)
+    if stream is not None:
+        with _current(stream):
+            return attention_backward(dout, q, k, v, out, lse, plan, scale, status)
     shape = plan.of(q, k, v)
+    device = _device(plan.buffer, dout, q, k, v, out, lse, status)
     for t, name in ((dout, "dout"), (out, "out")):
         if t.shape != q.shape or t.dtype != q.dtype:
             raise ValueError(f"{name}: q's shape and type are needed")
     if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse: the forward pass's float32 [rows][heads] is needed")
     dq, dk, dv = _like(q), _like(k), _like(v)
-    with torch.cuda.device(q.device):
-        B.vitfe_attention_backward(shape, plan.buffer, dout, _heads(dout, "dout"), q, _heads(q, "q"), k,
-                                   _heads(k, "k"), v, _heads(v, "v"), out, _heads(out, "out"), lse,
-                                   shape.head_dim ** -0.5 if scale is None else scale, dq, _heads(dq, "dq"), dk,
-                                   _heads(dk, "dk"), dv, _heads(dv, "dv"),
-                                   _work(B.vitfe_attention_backward_workspace(shape), q.device), status,
-                                   _on(q, stream))
+    work = torch.empty(plan._work_backward, dtype=torch.uint8, device=q.device) if plan._work_backward else None
+    _launch("vitfe_attention_backward", device, shape, plan.buffer.data_ptr(), dout.data_ptr(), _heads(dout, "dout"),
+            q.data_ptr(), _heads(q, "q"), k.data_ptr(), _heads(k, "k"), v.data_ptr(), _heads(v, "v"), out.data_ptr(),
+            _heads(out, "out"), lse.data_ptr(), q.shape[2] ** -0.5 if scale is None else scale, dq.data_ptr(),
+            _heads(dq, "dq"), dk.data_ptr(), _heads(dk, "dk"), dv.data_ptr(), _heads(dv, "dv"), _ptr(work),
+            _ptr(status))
     return dq, dk, dv
 
 
