@@ -446,11 +446,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // ------------------------------------------------------------- loads
     if (lane == 0) {
       uint32_t nq[2] = {0, 0}, nk = 0;
+      RingPos pos;
       bool ok = true;
       const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
       auto load = [&](const CUtensorMap* map, int head, int key) {
-        const uint32_t st = nk % (uint32_t)stages, ph = (nk / (uint32_t)stages) & 1u;
-        if (!mbar_wait(smem_u32(&sh.kv_empty[st]), ph ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        const uint32_t st = pos.i;
+        if (!mbar_wait(smem_u32(&sh.kv_empty[st]), pos.parity ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        pos = pos.next((uint32_t)stages);
         const uint32_t bar = smem_u32(&sh.kv_full[st]);
         mbar_arrive_expect_tx(bar, tile_bytes);
         for (int b = 0; b < nb; ++b)
@@ -501,91 +503,91 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t id_s = idesc_16<T>(128, kAttnKeys, false);
     const uint32_t id_o = idesc_16<T>(128, (d + 15) / 16 * 16, true);
     const int ksteps = (d + 15) / 16;
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, nk = 0;
+    const uint64_t q_desc = sw128_desc(tiles), k_desc = sw128_desc(ring), v_desc = sw128_desc_rows(ring);
+    const uint64_t tile_step = (uint64_t)(tile_bytes >> 4);
+    const uint32_t nst = (uint32_t)stages;
+    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+    RingPos kp, vp = kp.next(nst);                // the next K and V tile: K0 V0 K1 V1 ...
     bool ok = true;
-    auto stage_of = [&](uint32_t i) { return i % (uint32_t)stages; };
-    auto wait_kv = [&](uint32_t i) {
-      if (!mbar_wait_warp<false>(smem_u32(&sh.kv_full[stage_of(i)]), (i / (uint32_t)stages) & 1u, abort_flag, kAttnWaitNs))
-        ok = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
       return ok;
     };
-    auto scores = [&](int t, uint32_t kst) {      // S_t = Q_t K^T, announced on s_full
+    // S_t = Q_t K^T, announced on s_full; then `also` and `release`, when given
+    auto scores = [&](int t, uint32_t st, uint64_t* also, uint64_t* release) {
       if (elect_one()) {
-        const uint64_t qd = sw128_desc(tiles + (uint32_t)t * tile_bytes), kd = sw128_desc(ring + kst * tile_bytes);
-        for (int k = 0; k < ksteps; ++k) {
-          const uint64_t o = (uint64_t)((k >> 2) * (kColBlockBytes >> 4) + (k & 3) * 2);
-          umma_bf16(tmem + (uint32_t)t * 128u, qd + o, kd + o, id_s, k > 0);
-        }
+        issue_scores(tmem + (uint32_t)t * 128u, q_desc + (uint64_t)t * tile_step, k_desc + st * tile_step, id_s, ksteps);
         umma_commit(smem_u32(&sh.s_full[t]));
+        if (also) umma_commit(smem_u32(also));
+        if (release) umma_commit(smem_u32(release));
       }
       __syncwarp();
     };
-    auto output = [&](int t, uint32_t vst, bool first) {      // O_t (+)= P_t V
+    auto output = [&](int t, uint32_t st, bool first, uint64_t* also, uint64_t* release) {      // O_t (+)= P_t V
       if (elect_one()) {
-        const uint64_t vd = sw128_desc_rows(ring + vst * tile_bytes);
-#pragma unroll
-        for (int k = 0; k < kAttnKeys / 16; ++k)
-          umma_ta(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + 8u * k, vd + (uint64_t)(128 * k), id_o,
-                  !first || k > 0);
+        issue_sum(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u, 0, v_desc + st * tile_step, id_o, !first);
+        if (also) umma_commit(smem_u32(also));
+        if (release) umma_commit(smem_u32(release));
       }
-      __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(smem_u32(bar));
       __syncwarp();
     };
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnItem it = items[w / hk];
-      const int nt[2] = {tile_blocks(it, 0, tok, causal), tile_blocks(it, 1, tok, causal)};
-      const int n = max(nt[0], nt[1]);
+      const int n0 = uniform(tile_blocks(it, 0, tok, causal)), n1 = uniform(tile_blocks(it, 1, tok, causal));
+      const int n = max(n0, n1), keys = uniform(it.kn - it.kb * kAttnKeys);
       if (n == 0) continue;
-      uint32_t ik = nk, iv = nk + 1;              // ring indexes of K(j), V(j): K0 V0 K1 V1 ...
-      if (!wait_kv(ik)) break;
-      for (int t = 0; ok && t < 2; ++t) {
-        if (nt[t] == 0) continue;
-        if (!mbar_wait_warp<false>(smem_u32(&sh.q_full[t]), nq[t] & 1u, abort_flag, kAttnWaitNs)) ok = false;
-        else {
-          ++nq[t];
-          scores(t, stage_of(ik));
-          if (nt[t] == 1) commit(&sh.q_empty[t]);
+      if (!wait(&sh.kv_full[kp.i], kp.parity)) break;
+      if (n0 > 0) {
+        if (!wait(&sh.q_full[0], nq[0]++ & 1u)) break;
+        scores(0, kp.i, n0 == 1 ? &sh.q_empty[0] : nullptr, n1 == 0 ? &sh.kv_empty[kp.i] : nullptr);
+      }
+      if (n1 > 0) {
+        if (!wait(&sh.q_full[1], nq[1]++ & 1u)) break;
+        scores(1, kp.i, n1 == 1 ? &sh.q_empty[1] : nullptr, &sh.kv_empty[kp.i]);
+      }
+      for (int j = 0; j < n; ++j) {
+        const RingPos kn = vp.next(nst), vn = kn.next(nst);      // K(j + 1), V(j + 1)
+        const bool more = j + 1 < n;
+        bool v_here = false, k_here = false;
+        // which tile is the last to read V(j), K(j + 1)
+        const bool v_last1 = j < n1, k_last1 = j + 1 < n1;
+        auto v_wait = [&]() {
+          if (v_here) return true;
+          if (!wait(&sh.kv_full[vp.i], vp.parity)) return false;
+          const int have = keys - j * kAttnKeys;        // rows past the sequence's end weigh 0 in P,
+          if (have < kAttnKeys) zero_tile_rows(ring + vp.i * tile_bytes, nb, have);   // but 0 * NaN is NaN
+          return v_here = true;
+        };
+        auto k_wait = [&]() { return k_here || (k_here = wait(&sh.kv_full[kn.i], kn.parity)); };
+        if (j < n0) {
+          if (!wait(&sh.p_full[0], np[0]++ & 1u) || !v_wait()) break;
+          tc_fence_after();
+          output(0, vp.i, j == 0, j + 1 == n0 ? &sh.o_full[0] : nullptr, v_last1 ? nullptr : &sh.kv_empty[vp.i]);
+          if (j + 1 < n0) {
+            if (!k_wait()) break;
+            scores(0, kn.i, j + 2 == n0 ? &sh.q_empty[0] : nullptr, k_last1 ? nullptr : &sh.kv_empty[kn.i]);
+          }
+        }
+        if (j < n1) {
+          if (!wait(&sh.p_full[1], np[1]++ & 1u) || !v_wait()) break;
+          tc_fence_after();
+          output(1, vp.i, j == 0, j + 1 == n1 ? &sh.o_full[1] : nullptr, &sh.kv_empty[vp.i]);
+          if (j + 1 < n1) {
+            if (!k_wait()) break;
+            scores(1, kn.i, j + 2 == n1 ? &sh.q_empty[1] : nullptr, &sh.kv_empty[kn.i]);
+          }
+        }
+        if (more) {
+          kp = kn;
+          vp = vn;
         }
       }
       if (!ok) break;
-      commit(&sh.kv_empty[stage_of(ik)]);
-      for (int j = 0; ok && j < n; ++j) {
-        const bool more = j + 1 < n;
-        for (int t = 0; ok && t < 2; ++t) {
-          if (j >= nt[t]) continue;
-          if (!mbar_wait_warp<false>(smem_u32(&sh.p_full[t]), np[t] & 1u, abort_flag, kAttnWaitNs)) {
-            ok = false;
-            break;
-          }
-          ++np[t];
-          tc_fence_after();
-          if (t == 0 || nt[0] <= j) {
-            if (!wait_kv(iv)) break;
-            const int have = it.kn - (it.kb + j) * kAttnKeys;   // rows past the sequence's end weigh 0 in P,
-            if (have < kAttnKeys) zero_tile_rows(ring + stage_of(iv) * tile_bytes, nb, have);   // but 0 * NaN is NaN
-          }
-          output(t, stage_of(iv), j == 0);
-          if (j + 1 == nt[t]) {
-            commit(&sh.o_full[t]);
-          } else {
-            if ((t == 0 || nt[0] <= j + 1) && !wait_kv(ik + 2)) break;
-            scores(t, stage_of(ik + 2));
-            if (j + 2 == nt[t]) commit(&sh.q_empty[t]);
-          }
-        }
-        if (!ok) break;
-        commit(&sh.kv_empty[stage_of(iv)]);
-        if (more) commit(&sh.kv_empty[stage_of(ik + 2)]);
-        ik += 2;
-        iv += 2;
-      }
-      nk += 2u * (uint32_t)n;
+      kp = vp.next(nst);
+      vp = kp.next(nst);
     }
     if (!ok) {      // matrix instructions in flight end on their own: wait for them
-      commit(&sh.drain);
+      if (elect_one()) umma_commit(smem_u32(&sh.drain));
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(smem_u32(&sh.drain), 0) && global_timer_ns() - t0 < kAttnWaitNs) {
       }

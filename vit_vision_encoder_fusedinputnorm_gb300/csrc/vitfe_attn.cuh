@@ -182,6 +182,42 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A value that is the same in all lanes, in a form that the compiler takes as such: loop bounds and
+// addresses of the issuing warp then stay in uniform registers, where the matrix instructions want
+// their operands (moving each one there costs more than the instruction's own issue).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// A position in a ring of `n` slots: index and the parity of its use.
+struct RingPos {
+  uint32_t i = 0, parity = 0;
+  __device__ __forceinline__ RingPos next(uint32_t n) const {
+    RingPos r;
+    const bool wrap = i + 1 == n;
+    r.i = wrap ? 0u : i + 1;
+    r.parity = wrap ? parity ^ 1u : parity;
+    return r;
+  }
+};
+
+// S or dP: D = A B^T over the head's columns, both tiles K-major in shared memory.  `ksteps`: steps of
+// 16 columns, up to 8.
+__device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, int ksteps) {
+#pragma unroll
+  for (int k = 0; k < VITFE_ATTN_MAX_HEAD_DIM / 16; ++k) {
+    constexpr uint64_t block = kColBlockBytes >> 4;
+    const uint64_t o = (uint64_t)(k >> 2) * block + (uint64_t)(k & 3) * 2;
+    if (k < ksteps) umma_bf16(d_tmem, ad + o, bd + o, idesc, k > 0);
+  }
+}
+// O, dV, dK or dQ: D (+)= A B, A (128 x 128, 16-bit) in tensor memory, where the second 64 of its
+// contraction start `gap` columns after the first 64's 32, B read by rows.
+__device__ __forceinline__ void issue_sum(uint32_t d_tmem, uint32_t a_tmem, uint32_t gap, uint64_t bd, uint32_t idesc,
+                                          uint32_t accumulate) {
+#pragma unroll
+  for (int k = 0; k < kAttnKeys / 16; ++k)
+    umma_ta(d_tmem, a_tmem + 8u * k + (k < 4 ? 0u : gap), bd + (uint64_t)(128 * k), idesc, k > 0 ? 1u : accumulate);
+}
+
 // Zero rows [first, 128) of a tile of `blocks` column blocks (whole warp; the swizzle moves
 // 16-byte chunks inside a row only), visible to the tensor core that reads the tile next.
 __device__ __forceinline__ void zero_tile_rows(uint32_t tile, int blocks, int first) {
