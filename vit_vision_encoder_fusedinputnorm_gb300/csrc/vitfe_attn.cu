@@ -240,6 +240,10 @@ __global__ void status_ok_kernel(int32_t* status) {
 }
 
 constexpr int kFwdThreads = 384;
+// Registers a thread: the launch's, then the softmax warpgroups' and the third's.  The shares have to
+// add up to what the block was launched with, or the increase would wait for ever.
+constexpr int kFwdRegs = 168, kSoftRegs = 208, kIssueRegs = 88;
+static_assert(2 * kSoftRegs + kIssueRegs <= 3 * kFwdRegs, "");
 constexpr int kMaxStages = 10;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -313,6 +317,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax and output
+    more_registers<kSoftRegs>();
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (!live) lim = 0;
       float m = -INFINITY, l = 0.f;                          // m: the reference of the exponents
       for (int j = 0; j < n; ++j, ++ns) {
-        if (!mbar_wait_warp<false>(smem_u32(&sh.s_full[t]), ns & 1u, abort_flag, kAttnWaitNs)) {
+        if (!wait_inline(&sh.s_full[t], ns & 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -354,10 +359,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
+        for (int e = 0; e < 32; e += 2)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][e]));
-        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], m);
         // The exponents' reference moves only when the maximum has outgrown it by 2^8: until then
         // P is at most 2^8 and the fp32 sums hold it exactly as well, and O need not be touched.
         if (j == 0) {
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       if (!ok) break;
       if (n > 0) {
-        if (!mbar_wait_warp<false>(smem_u32(&sh.o_full[t]), no & 1u, abort_flag, kAttnWaitNs)) {
+        if (!wait_inline(&sh.o_full[t], no & 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -442,7 +447,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         else if (a.lse) a.lse[qrow * a.s.heads_q + head] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
       }
     }
-  } else if (warp == 8) {
+  } else {
+    fewer_registers<kIssueRegs>();
+  }
+  if (warp == 8) {
     // ------------------------------------------------------------- loads
     if (lane == 0) {
       uint32_t nq[2] = {0, 0}, nk = 0;
@@ -510,7 +518,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     RingPos kp, vp = kp.next(nst);                // the next K and V tile: K0 V0 K1 V1 ...
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
+      ok = ok && wait_inline(bar, parity, abort_flag);
       return ok;
     };
     // S_t = Q_t K^T, announced on s_full; then `also` and `release`, when given
@@ -671,7 +679,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   int sms = 0;
   cudaError_t e = current_sms(&sms);
   if (e == cudaSuccess)
-    e = allow_smem(reinterpret_cast<const void*>(attn_kernel<T>), kSmemMax - (int)sizeof(FwdShared), allowed);
+    e = allow_smem(reinterpret_cast<const void*>(attn_kernel<T>), kSmemMax - (int)sizeof(FwdShared), allowed, kFwdRegs);
   if (e != cudaSuccess) return e;
   const int64_t work = a.l.cap_items * s.heads_kv;
   attn_kernel<T><<<(unsigned)(work < sms ? work : sms), kFwdThreads, smem, st>>>(a, mq, mk, mv, stages);

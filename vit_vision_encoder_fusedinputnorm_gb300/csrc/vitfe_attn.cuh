@@ -177,6 +177,20 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The warpgroup's registers a thread from here on (all four warps; multiples of 8).
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -216,6 +230,20 @@ __device__ __forceinline__ void issue_sum(uint32_t d_tmem, uint32_t a_tmem, uint
 #pragma unroll
   for (int k = 0; k < kAttnKeys / 16; ++k)
     umma_ta(d_tmem, a_tmem + 8u * k + (k < 4 ? 0u : gap), bd + (uint64_t)(128 * k), idesc, k > 0 ? 1u : accumulate);
+}
+
+// mbar_wait_warp<false> all inline: a kernel that shares out its registers anew can hold no call.
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const uint32_t b = smem_u32(bar);
+  if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    if ((i & 15u) == 0 && __any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > kAttnWaitNs)) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
 }
 
 // Zero rows [first, 128) of a tile of `blocks` column blocks (whole warp; the swizzle moves

@@ -82,8 +82,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 // SMs of the current device, asked for once per device.
 cudaError_t current_sms(int* sms);
 // Allow `kernel` up to `smem` bytes of dynamic shared memory on the current device, once per device
-// (`done`: a bit for each device below 64, of this kernel alone).
-cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done);
+// (`done`: a bit for each device below 64, of this kernel alone).  `regs` > 0: the registers a thread
+// that the kernel has to be launched with (it shares them out anew); an error when it is not.
+cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done, int regs = 0);
 
 // ---------------------------------------------------------------------------
 // launchers

@@ -295,12 +295,18 @@ cudaError_t current_sms(int* sms) {
   return e;
 }
 
-cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done) {
+cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done, int regs) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (regs > 0) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != regs) return cudaErrorInvalidDeviceFunction;
+  }
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
