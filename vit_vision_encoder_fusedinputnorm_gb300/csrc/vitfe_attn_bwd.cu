@@ -14,10 +14,10 @@ constexpr int kMaxPairs = 4;         // ring stages
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Per query row and head: the exponents' reference and delta.  A row that sees no key (lse -inf)
-// gets +inf, so that its probabilities are 0.
+// Per query row and head, negated: the log-sum-exp as an exponent of 2, and delta.  A row that sees
+// no key (lse -inf) has -inf here, so that its probabilities are 0.
 struct alignas(8) RowValue {
-  float lse2, delta;
+  float nlse2, ndelta;
 };
 
 template <typename T>
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnArgs a) {
     for (int m = 8; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (i < n && sub == 0) {
       const float lse = a.lse[i];
-      rows[i] = RowValue{lse == -INFINITY ? INFINITY : lse * kLog2e, s};
+      rows[i] = RowValue{lse == -INFINITY ? -INFINITY : -(lse * kLog2e), -s};
     }
   }
 }
@@ -57,8 +57,8 @@ struct BwdShared {
   uint64_t s_full[2], dp_full, p_full, ds_full, acc_full, drain;
   uint32_t tmem;
   int abort;
-  alignas(16) RowValue rows[kMaxPairs][kAttnRows];
-  alignas(16) int last_key[kMaxPairs][kAttnRows];                 // the last local key that the row sees
+  alignas(16) float nlse2[kMaxPairs][kAttnRows], ndelta[kMaxPairs][kAttnRows];   // of a query tile's rows
+  alignas(16) int last_key[kMaxPairs][kAttnRows];                                // the last local key that one sees
 };
 
 __device__ __forceinline__ int deal(int round) {
@@ -130,25 +130,14 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
   for (int b = 0; b < nb; ++b) tma_load_3d(dst + (uint32_t)b * kColBlockBytes, map, bar, b * kColBlock, head, row);
 }
 
-// D = A B^T over the head's columns: both tiles K-major in shared memory.
-template <typename T>
-__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, int ksteps) {
-  const uint64_t ad = sw128_desc(a_tile), bd = sw128_desc(b_tile);
-  for (int k = 0; k < ksteps; ++k) {
-    const uint64_t o = (uint64_t)((k >> 2) * (kColBlockBytes >> 4) + (k & 3) * 2);
-    umma_bf16(d_tmem, ad + o, bd + o, idesc_16<T>(128, 128, false), k > 0);
-  }
+// 64 scores of a thread and the 64 values of a row vector, as pairs: the row vector is the same for
+// every lane, so shared memory serves four of its floats to the whole warp at once.
+__device__ __forceinline__ void load_scores(uint32_t col, uint32_t (&s)[64]) {
+  tmem_ld_32x32b_x32(col, *reinterpret_cast<uint32_t(*)[32]>(s));
+  tmem_ld_32x32b_x32(col + 32u, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+  tmem_wait_ld();
 }
-
-// D (+)= A B with A (128 x 128, 16-bit) in tensor memory: the first 64 columns of its contraction
-// packed from column `a_tmem` on, the other 64 from a_tmem + 64 on (each half of the score warps
-// writes over the columns that it read itself).
-__device__ __forceinline__ void mma_sum(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_tile, uint32_t id, bool first) {
-  const uint64_t bd = sw128_desc_rows(b_tile);
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    umma_ta(d_tmem, a_tmem + (uint32_t)(k < 4 ? 8 * k : 64 + 8 * (k - 4)), bd + (uint64_t)(128 * k), id, !first || k > 0);
-}
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* v) { return (uint64_t)v[0] | ((uint64_t)v[1] << 32); }
 
 // 16-bit rows of an accumulator, columns [c0, c1) in steps of 16, times `f`.
 template <typename T>
@@ -220,39 +209,49 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t c0 = lanes + 64u * half;
     const float scale2 = a.scale * kLog2e;
-    uint32_t i = 0, acc = 0;                         // tiles so far (phases and stages), finished items
+    const uint64_t sc = f32x2(scale2, scale2);
+    uint32_t i = 0, acc = 0;                         // tiles so far, finished items (phases)
+    RingPos pos;
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnKeyItem it = items[w / hk];
       const int kh = w % hk;
       const TileRange tr = query_tiles(it, tok);
       for (int q = 0; q < tr.n; ++q, ++i) {
-        const uint32_t stg = i % (uint32_t)pairs;
-        if (!mbar_wait_warp<false>(smem_u32(&sh.row_full[stg]), (i / (uint32_t)pairs) & 1u, abort_flag, kAttnWaitNs) ||
+        const uint32_t stg = pos.i;
+        if (!mbar_wait_warp<false>(smem_u32(&sh.row_full[stg]), pos.parity, abort_flag, kAttnWaitNs) ||
             !mbar_wait_warp<false>(smem_u32(&sh.s_full[0]), i & 1u, abort_flag, kAttnWaitNs)) {
           ok = false;
           break;
         }
+        pos = pos.next((uint32_t)pairs);
         tc_fence_after();
-        uint32_t s[64];
-        tmem_ld_32x32b_x32(st_col + c0, *reinterpret_cast<uint32_t(*)[32]>(s));
-        tmem_ld_32x32b_x32(st_col + c0 + 32u, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-        tmem_wait_ld();
+        uint32_t s[64], pk[32];
+        load_scores(st_col + c0, s);
         const int t = tr.t0 + q * tok;
         // every row of the tile is there and sees every key
         const bool whole = t + tok <= it.qn && it.off >= it.kn - 1 - t;
-        const RowValue* rv = sh.rows[stg] + 64 * half;
-        const int* lk = sh.last_key[stg] + 64 * half;
+        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sh.nlse2[stg] + 64 * half);
+        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sh.ndelta[stg] + 64 * half);
+        const int4* lk = reinterpret_cast<const int4*>(sh.last_key[stg] + 64 * half);
 #pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const float x = fmaf(__uint_as_float(s[e]), scale2, -rv[e].lse2);
-          s[e] = __float_as_uint(exp2_approx(x));
+        for (int e = 0; e < 64; e += 4) {
+          const ulonglong2 v = nl[e >> 2];
+          const uint64_t x = fma_f32x2(pair_of(s + e), sc, v.x), y = fma_f32x2(pair_of(s + e + 2), sc, v.y);
+          s[e] = __float_as_uint(exp2_approx(lo_f32(x)));
+          s[e + 1] = __float_as_uint(exp2_approx(hi_f32(x)));
+          s[e + 2] = __float_as_uint(exp2_approx(lo_f32(y)));
+          s[e + 3] = __float_as_uint(exp2_approx(hi_f32(y)));
         }
         if (!whole) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (key > lk[e]) s[e] = 0;
+          for (int e = 0; e < 64; e += 4) {
+            const int4 last = lk[e >> 2];
+            s[e] = key > last.x ? 0u : s[e];
+            s[e + 1] = key > last.y ? 0u : s[e + 1];
+            s[e + 2] = key > last.z ? 0u : s[e + 2];
+            s[e + 3] = key > last.w ? 0u : s[e + 3];
+          }
         }
-        uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 2) pk[e >> 1] = pack2<T>(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         tmem_st_32x32b_x32(st_col + c0, pk);
@@ -271,9 +270,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tmem_ld_32x32b_x32(dpt_col + c0 + 32u * c, dp);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float ds = __uint_as_float(s[32 * c + e]) * (__uint_as_float(dp[e]) - rv[32 * c + e].delta);
-            dp[e] = !whole && key > lk[32 * c + e] ? 0u : __float_as_uint(ds);
+          for (int e = 0; e < 32; e += 4) {
+            const ulonglong2 v = nd[8 * c + (e >> 2)];
+            const uint64_t x = mul_f32x2(pair_of(s + 32 * c + e), add_f32x2(pair_of(dp + e), v.x));
+            const uint64_t y = mul_f32x2(pair_of(s + 32 * c + e + 2), add_f32x2(pair_of(dp + e + 2), v.y));
+            dp[e] = (uint32_t)x;
+            dp[e + 1] = (uint32_t)(x >> 32);
+            dp[e + 2] = (uint32_t)y;
+            dp[e + 3] = (uint32_t)(y >> 32);
+          }
+          if (!whole) {      // a hidden pair counts nothing, whatever dP holds there
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const int4 last = lk[8 * c + (e >> 2)];
+              dp[e] = key > last.x ? 0u : dp[e];
+              dp[e + 1] = key > last.y ? 0u : dp[e + 1];
+              dp[e + 2] = key > last.z ? 0u : dp[e + 2];
+              dp[e + 3] = key > last.w ? 0u : dp[e + 3];
+            }
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) pk[16 * c + (e >> 1)] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
@@ -333,108 +347,106 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    const uint32_t id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
+    const uint32_t id_s = idesc_16<T>(128, 128, false), id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
     const int ksteps = (d + 15) / 16;
-    const uint32_t stages = 2u * (uint32_t)pairs;
+    const uint32_t npairs = (uint32_t)pairs;
+    const uint64_t tile_step = (uint64_t)(tile_bytes >> 4), pair_step = 2 * tile_step;
+    const uint64_t k_desc = sw128_desc(tiles), v_desc = k_desc + tile_step;
+    const uint64_t q_cols = sw128_desc(ring), do_cols = q_cols + tile_step;               // contraction: columns
+    const uint64_t q_rows = sw128_desc_rows(ring), do_rows = q_rows + tile_step;          // contraction: rows
     uint32_t i = 0, np = 0;
-    auto tile = [&](uint32_t n) { return ring + (n % stages) * tile_bytes; };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(smem_u32(bar));
-      __syncwarp();
+    RingPos pos;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
+      return ok;
     };
-    // the n-th ring tile has landed; rows past the sequence's end are zeroed (they belong to others,
-    // and 0 * NaN is NaN)
-    auto wait_tile = [&](uint32_t n, int have) {
-      if (!mbar_wait_warp<false>(smem_u32(&sh.full[n % stages]), (n / stages) & 1u, abort_flag, kAttnWaitNs)) return false;
-      if (have < tok) zero_tile_rows(tile(n), nb, have * g);
+    // tile `which` (0: Q, 1: dO) of a pair has landed; rows past the sequence's end are zeroed (they
+    // belong to others, and 0 * NaN is NaN)
+    auto wait_tile = [&](const RingPos& p, uint32_t which, int have) {
+      if (!wait(&sh.full[2 * p.i + which], p.parity)) return false;
+      if (have < tok) zero_tile_rows(ring + (2 * p.i + which) * tile_bytes, nb, have * g);
       return true;
-    };
-    auto scores = [&](uint32_t n, uint32_t resident, uint32_t d_col, uint64_t* bar) {
-      if (elect_one()) {
-        mma_scores<T>(d_col, resident, tile(n), ksteps);
-        umma_commit(smem_u32(bar));
-      }
-      __syncwarp();
-    };
-    auto sum = [&](uint32_t d_col, uint32_t a_col, uint32_t n, bool first) {
-      if (elect_one()) mma_sum(d_col, a_col, tile(n), id_acc, first);
-      __syncwarp();
     };
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnKeyItem it = items[w / hk];
       const TileRange tr = query_tiles(it, tok);
-      if (tr.n == 0) continue;
-      auto have = [&](int q) { return it.qn - (tr.t0 + q * tok); };
-      ok = mbar_wait_warp<false>(smem_u32(&sh.kv_full), np & 1u, abort_flag, kAttnWaitNs);
-      ++np;
-      if (ok) ok = wait_tile(2 * i, have(0));
-      if (ok) scores(2 * i, tiles, st_col, &sh.s_full[0]);
-      if (ok) ok = wait_tile(2 * i + 1, have(0));
-      if (ok) scores(2 * i + 1, tiles + tile_bytes, dpt_col, &sh.dp_full);
-      for (int q = 0; ok && q < tr.n; ++q, ++i) {
-        const bool more = q + 1 < tr.n;
-        if (!mbar_wait_warp<false>(smem_u32(&sh.p_full), i & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
+      const int n = uniform(tr.n), rows0 = uniform(it.qn - tr.t0);     // tokens from the first tile on
+      if (n == 0) continue;
+      if (!wait(&sh.kv_full, np++ & 1u) || !wait_tile(pos, 0, rows0)) break;
+      if (elect_one()) {
+        issue_scores(st_col, k_desc, q_cols + pos.i * pair_step, id_s, ksteps);
+        umma_commit(smem_u32(&sh.s_full[0]));
+      }
+      __syncwarp();
+      if (!wait_tile(pos, 1, rows0)) break;
+      if (elect_one()) {
+        issue_scores(dpt_col, v_desc, do_cols + pos.i * pair_step, id_s, ksteps);
+        umma_commit(smem_u32(&sh.dp_full));
+      }
+      __syncwarp();
+      for (int q = 0; q < n; ++q, ++i) {
+        const bool more = q + 1 < n;
+        const int have = rows0 - (q + 1) * tok;
+        const RingPos nx = pos.next(npairs);
+        if (more && !wait_tile(nx, 0, have)) break;
+        if (!wait(&sh.p_full, i & 1u)) break;
         tc_fence_after();
-        sum(dv_col, st_col, 2 * i + 1, q == 0);                     // dV += P^T dO
-        if (more) {
-          if (!wait_tile(2 * i + 2, have(q + 1))) {
-            ok = false;
-            break;
+        if (elect_one()) {
+          issue_sum(dv_col, st_col, 32, do_rows + pos.i * pair_step, id_acc, q > 0);             // dV += P^T dO
+          if (more) {
+            issue_scores(st_col, k_desc, q_cols + nx.i * pair_step, id_s, ksteps);
+            umma_commit(smem_u32(&sh.s_full[0]));
           }
-          scores(2 * i + 2, tiles, st_col, &sh.s_full[0]);
         }
-        if (!mbar_wait_warp<false>(smem_u32(&sh.ds_full), i & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
+        __syncwarp();
+        if (more && !wait_tile(nx, 1, have)) break;
+        if (!wait(&sh.ds_full, i & 1u)) break;
         tc_fence_after();
-        sum(dk_col, dpt_col, 2 * i, q == 0);                        // dK += dS^T Q
-        commit(&sh.empty[(2 * i) % stages]);
-        commit(&sh.empty[(2 * i + 1) % stages]);
-        if (more) {
-          if (!wait_tile(2 * i + 3, have(q + 1))) {
-            ok = false;
-            break;
+        if (elect_one()) {
+          issue_sum(dk_col, dpt_col, 32, q_rows + pos.i * pair_step, id_acc, q > 0);             // dK += dS^T Q
+          umma_commit(smem_u32(&sh.empty[2 * pos.i]));
+          umma_commit(smem_u32(&sh.empty[2 * pos.i + 1]));
+          if (more) {
+            issue_scores(dpt_col, v_desc, do_cols + nx.i * pair_step, id_s, ksteps);
+            umma_commit(smem_u32(&sh.dp_full));
+          } else {
+            umma_commit(smem_u32(&sh.acc_full));
+            umma_commit(smem_u32(&sh.kv_empty));
           }
-          scores(2 * i + 3, tiles + tile_bytes, dpt_col, &sh.dp_full);
-        } else {
-          commit(&sh.acc_full);
-          commit(&sh.kv_empty);
         }
+        __syncwarp();
+        pos = nx;
       }
     }
     if (!ok) drain_mma(sh);
   } else if (warp == 10) {
     // each query tile's row values beside it
     const RowValue* rows = static_cast<const RowValue*>(a.workspace);
-    const uint32_t stages = 2u * (uint32_t)pairs;
-    uint32_t i = 0;
+    RingPos pos;
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnKeyItem it = items[w / hk];
       const int kh = w % hk;
       const TileRange tr = query_tiles(it, tok);
-      for (int q = 0; q < tr.n; ++q, ++i) {
-        const uint32_t stg = i % (uint32_t)pairs;
+      for (int q = 0; q < tr.n; ++q) {
+        const uint32_t stg = pos.i;
         // free when the matrix instructions on the same pair are done
-        if (!mbar_wait_warp<false>(smem_u32(&sh.empty[(2 * i + 1) % stages]), ((i / (uint32_t)pairs) & 1u) ^ 1u, abort_flag,
-                                   kAttnWaitNs)) {
+        if (!mbar_wait_warp<false>(smem_u32(&sh.empty[2 * stg + 1]), pos.parity ^ 1u, abort_flag, kAttnWaitNs)) {
           ok = false;
           break;
         }
+        pos = pos.next((uint32_t)pairs);
         const int t = tr.t0 + q * tok;
 #pragma unroll
         for (int c = 0; c < kAttnRows; c += 32) {
           const int x = c + lane, tt = t + x / g;
-          RowValue v{INFINITY, 0.f};
+          RowValue v{-INFINITY, 0.f};
           int last = -1;
           if (x < tok * g && tt < it.qn) {
             v = rows[((int64_t)it.q0 + tt) * a.s.heads_q + kh * g + x % g];
             last = tt + it.off;
           }
-          sh.rows[stg][x] = v;
+          sh.nlse2[stg][x] = v.nlse2;
+          sh.ndelta[stg][x] = v.ndelta;
           sh.last_key[stg][x] = last;
         }
         __syncwarp();
@@ -490,6 +502,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float scale2 = a.scale * kLog2e;
+    const uint64_t sc = f32x2(scale2, scale2);
     const RowValue* rows = static_cast<const RowValue*>(a.workspace);
     uint32_t i = 0, acc = 0;
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
@@ -500,9 +513,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int my_tok = t * tok + row / g, head = kh * g + row % g;
       const bool live = row < tok * g && my_tok < it.qn;
       int lim = causal ? min(it.kn, it.off + my_tok + 1) : it.kn;
-      RowValue v{INFINITY, 0.f};
+      RowValue v{-INFINITY, 0.f};
       if (live) v = rows[((int64_t)it.q0 + my_tok) * a.s.heads_q + head];
       else lim = 0;
+      const uint64_t nl = f32x2(v.nlse2, v.nlse2), nd = f32x2(v.ndelta, v.ndelta);
       for (int j = 0; j < n; ++j, ++i) {
         const uint32_t s_col = tmem + lanes + (i & 1u) * 128u + 64u * half;
         if (!mbar_wait_warp<false>(smem_u32(&sh.s_full[i & 1u]), (i >> 1) & 1u, abort_flag, kAttnWaitNs)) {
@@ -510,29 +524,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t s[64];
-        tmem_ld_32x32b_x32(s_col, *reinterpret_cast<uint32_t(*)[32]>(s));
-        tmem_ld_32x32b_x32(s_col + 32u, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-        tmem_wait_ld();
+        uint32_t s[64], pk[32];
+        load_scores(s_col, s);
         const int left = lim - j * kAttnKeys - 64 * half;
         const bool whole = __all_sync(0xffffffffu, left >= 64);
 #pragma unroll
-        for (int e = 0; e < 64; ++e) s[e] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(s[e]), scale2, -v.lse2)));
+        for (int e = 0; e < 64; e += 2) {
+          const uint64_t x = fma_f32x2(pair_of(s + e), sc, nl);
+          s[e] = __float_as_uint(exp2_approx(lo_f32(x)));
+          s[e + 1] = __float_as_uint(exp2_approx(hi_f32(x)));
+        }
         if (!mbar_wait_warp<false>(smem_u32(&sh.dp_full), i & 1u, abort_flag, kAttnWaitNs)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t dp[32];
           tmem_ld_32x32b_x32(dp_col + lanes + 64u * half + 32u * c, dp);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float ds = __uint_as_float(s[32 * c + e]) * (__uint_as_float(dp[e]) - v.delta);
-            dp[e] = !whole && 32 * c + e >= left ? 0u : __float_as_uint(ds);
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t x = mul_f32x2(pair_of(s + 32 * c + e), add_f32x2(pair_of(dp + e), nd));
+            dp[e] = (uint32_t)x;
+            dp[e + 1] = (uint32_t)(x >> 32);
+          }
+          if (!whole) {      // a hidden key counts nothing, whatever dP holds there
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= left) dp[e] = 0u;
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) pk[16 * c + (e >> 1)] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
@@ -592,69 +613,61 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    const uint32_t id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
+    const uint32_t id_s = idesc_16<T>(128, 128, false), id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
     const int ksteps = (d + 15) / 16;
+    const uint32_t npairs = (uint32_t)pairs;
+    const uint64_t tile_step = (uint64_t)(tile_bytes >> 4), pair_step = 2 * tile_step;
+    const uint64_t q_desc = sw128_desc(tiles), do_desc = q_desc + tile_step;
+    const uint64_t k_cols = sw128_desc(ring), v_cols = k_cols + tile_step, k_rows = sw128_desc_rows(ring);
     uint32_t i = 0, np = 0;
-    auto tile = [&](uint32_t n) { return ring + (n % stages) * tile_bytes; };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(smem_u32(bar));
-      __syncwarp();
+    RingPos pos;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
+      return ok;
     };
-    auto wait_tile = [&](uint32_t n) {
-      return mbar_wait_warp<false>(smem_u32(&sh.full[n % stages]), (n / stages) & 1u, abort_flag, kAttnWaitNs);
+    // S of the block at p into buffer b; K rows past the sequence's end are zeroed for dQ += dS K
+    auto s_of = [&](const RingPos& p, uint32_t b, int have) {
+      if (!wait(&sh.full[2 * p.i], p.parity)) return false;
+      if (have < kAttnKeys) zero_tile_rows(ring + 2 * p.i * tile_bytes, nb, have);
+      if (elect_one()) {
+        issue_scores(tmem + b * 128u, q_desc, k_cols + p.i * pair_step, id_s, ksteps);
+        umma_commit(smem_u32(&sh.s_full[b]));
+      }
+      __syncwarp();
+      return true;
     };
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnItem it = items[w / (2 * hk)];
-      const int n = key_blocks(it, w & 1, tok, causal);
+      const int n = uniform(key_blocks(it, w & 1, tok, causal)), keys = uniform(it.kn);
       if (n == 0) continue;
-      // S(j), into buffer (i + j) & 1; K rows past the sequence's end are zeroed for dQ += dS K
-      auto s_of = [&](int j, uint32_t ii) {
-        if (!wait_tile(2 * ii)) return false;
-        const int have = it.kn - j * kAttnKeys;
-        if (have < kAttnKeys) zero_tile_rows(tile(2 * ii), nb, have);
-        if (elect_one()) {
-          mma_scores<T>(tmem + (ii & 1u) * 128u, tiles, tile(2 * ii), ksteps);
-          umma_commit(smem_u32(&sh.s_full[ii & 1u]));
-        }
-        __syncwarp();
-        return true;
-      };
-      auto dp_of = [&](uint32_t ii) {
-        if (!wait_tile(2 * ii + 1)) return false;
-        if (elect_one()) {
-          mma_scores<T>(dp_col, tiles + tile_bytes, tile(2 * ii + 1), ksteps);
-          umma_commit(smem_u32(&sh.dp_full));
-          umma_commit(smem_u32(&sh.empty[(2 * ii + 1) % stages]));
-        }
-        __syncwarp();
-        return true;
-      };
-      ok = mbar_wait_warp<false>(smem_u32(&sh.kv_full), np & 1u, abort_flag, kAttnWaitNs);
-      ++np;
-      if (ok) ok = s_of(0, i) && dp_of(i);
-      for (int j = 0; ok && j < n; ++j, ++i) {
-        if (j + 1 < n && !s_of(j + 1, i + 1)) {
-          ok = false;
-          break;
-        }
-        if (!mbar_wait_warp<false>(smem_u32(&sh.ds_full), i & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
+      if (!wait(&sh.kv_full, np++ & 1u) || !s_of(pos, i & 1u, keys) || !wait(&sh.full[2 * pos.i + 1], pos.parity)) break;
+      if (elect_one()) {
+        issue_scores(dp_col, do_desc, v_cols + pos.i * pair_step, id_s, ksteps);
+        umma_commit(smem_u32(&sh.dp_full));
+        umma_commit(smem_u32(&sh.empty[2 * pos.i + 1]));
+      }
+      __syncwarp();
+      for (int j = 0; j < n; ++j, ++i) {
+        const bool more = j + 1 < n;
+        const RingPos nx = pos.next(npairs);
+        if (more && (!s_of(nx, (i + 1) & 1u, keys - (j + 1) * kAttnKeys) || !wait(&sh.full[2 * nx.i + 1], nx.parity))) break;
+        if (!wait(&sh.ds_full, i & 1u)) break;
         tc_fence_after();
-        if (j + 1 < n && !dp_of(i + 1)) {
-          ok = false;
-          break;
-        }
         if (elect_one()) {
-          mma_sum(dq_col, tmem + (i & 1u) * 128u, tile(2 * i), id_acc, j == 0);
-          umma_commit(smem_u32(&sh.empty[(2 * i) % stages]));
+          if (more) {
+            issue_scores(dp_col, do_desc, v_cols + nx.i * pair_step, id_s, ksteps);
+            umma_commit(smem_u32(&sh.dp_full));
+            umma_commit(smem_u32(&sh.empty[2 * nx.i + 1]));
+          }
+          issue_sum(dq_col, tmem + (i & 1u) * 128u, 32, k_rows + pos.i * pair_step, id_acc, j > 0);    // dQ += dS K
+          umma_commit(smem_u32(&sh.empty[2 * pos.i]));
+          if (!more) {
+            umma_commit(smem_u32(&sh.acc_full));
+            umma_commit(smem_u32(&sh.kv_empty));
+          }
         }
         __syncwarp();
-        if (j + 1 == n) {
-          commit(&sh.acc_full);
-          commit(&sh.kv_empty);
-        }
+        pos = nx;
       }
     }
     if (!ok) drain_mma(sh);
