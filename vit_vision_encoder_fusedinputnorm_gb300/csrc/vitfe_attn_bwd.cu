@@ -10,7 +10,8 @@ namespace vitfe {
 namespace {
 
 constexpr int kBwdThreads = 384;     // 8 warps on scores, then loads, matrix instructions, row values, idle
-constexpr int kMaxPairs = 4;         // ring stages
+constexpr int kMaxSlots = 4;         // of each ring
+constexpr int kRowSlots = 2;         // of the row values
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -50,16 +51,23 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnArgs a) {
   }
 }
 
+// The slots of the two rings.  Ring A holds the tiles that a step's last product still reads (Q for
+// dK, K for dQ): its next tile is wanted a step early, so it is the deeper one.
+struct RingSizes {
+  uint32_t a, b;
+};
+
 struct BwdShared {
   uint64_t kv_full, kv_empty;                         // the resident pair of tiles
-  uint64_t full[2 * kMaxPairs], empty[2 * kMaxPairs]; // the ring
-  uint64_t row_full[kMaxPairs];
+  uint64_t a_full[kMaxSlots], a_empty[kMaxSlots], b_full[kMaxSlots], b_empty[kMaxSlots];
+  uint64_t row_full[kRowSlots], row_empty[kRowSlots];
   uint64_t s_full[2], dp_full, p_full, ds_full, acc_full, drain;
   uint32_t tmem;
   int abort;
-  alignas(16) float nlse2[kMaxPairs][kAttnRows], ndelta[kMaxPairs][kAttnRows];   // of a query tile's rows
-  alignas(16) int last_key[kMaxPairs][kAttnRows];                                // the last local key that one sees
+  alignas(16) float nlse2[kRowSlots][kAttnRows], ndelta[kRowSlots][kAttnRows];   // of a query tile's rows
 };
+// With two column blocks to a tile, seven tiles and this fill an SM's shared memory to the byte.
+static_assert(sizeof(BwdShared) <= 3072, "");
 
 __device__ __forceinline__ int deal(int round) {
   return round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
@@ -70,11 +78,16 @@ __device__ __forceinline__ void bwd_init(BwdShared& sh) {
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh.kv_full), 1);
     mbar_init(smem_u32(&sh.kv_empty), 1);
-    for (int i = 0; i < 2 * kMaxPairs; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
-      mbar_init(smem_u32(&sh.empty[i]), 1);
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(smem_u32(&sh.a_full[i]), 1);
+      mbar_init(smem_u32(&sh.a_empty[i]), 1);
+      mbar_init(smem_u32(&sh.b_full[i]), 1);
+      mbar_init(smem_u32(&sh.b_empty[i]), 1);
     }
-    for (int i = 0; i < kMaxPairs; ++i) mbar_init(smem_u32(&sh.row_full[i]), 1);
+    for (int i = 0; i < kRowSlots; ++i) {
+      mbar_init(smem_u32(&sh.row_full[i]), 1);
+      mbar_init(smem_u32(&sh.row_empty[i]), 8);
+    }
     mbar_init(smem_u32(&sh.s_full[0]), 1);
     mbar_init(smem_u32(&sh.s_full[1]), 1);
     mbar_init(smem_u32(&sh.dp_full), 1);
@@ -105,14 +118,12 @@ __device__ __forceinline__ void bwd_end(BwdShared& sh, uint32_t tmem, int32_t* s
   }
 }
 
-// After an abort: this thread's last loads (n into the ring, `pairs` into the resident tiles) land on
-// their own; wait for them before the CTA ends.
-__device__ __forceinline__ void drain_loads(BwdShared& sh, uint32_t n, uint32_t stages, uint32_t pairs) {
+// After an abort: the loads of one ring, or of the resident tiles, land on their own; wait for the last
+// `n` uses of the slots at `full` before the CTA ends.
+__device__ __forceinline__ void drain_loads(uint64_t* full, uint32_t n, uint32_t slots) {
   const uint64_t t0 = global_timer_ns();
-  while (pairs > 0 && !mbar_try_wait(smem_u32(&sh.kv_full), (pairs - 1) & 1u) && global_timer_ns() - t0 < kAttnWaitNs) {
-  }
-  for (uint32_t i = n - (n < stages ? n : stages); i < n; ++i)
-    while (!mbar_try_wait(smem_u32(&sh.full[i % stages]), (i / stages) & 1u) && global_timer_ns() - t0 < kAttnWaitNs) {
+  for (uint32_t i = n - (n < slots ? n : slots); i < n; ++i)
+    while (!mbar_try_wait(smem_u32(&full[i % slots]), (i / slots) & 1u) && global_timer_ns() - t0 < kAttnWaitNs) {
     }
 }
 
@@ -172,7 +183,7 @@ __device__ __forceinline__ TileRange query_tiles(const AttnKeyItem& it, int tok)
 }
 
 // ---------------------------------------------------------------------------
-// dk, dv.  Resident: the tiles of K and V.  Ring: pairs (Q, dO).  Scores are transposed (lane = key),
+// dk, dv.  Resident: the tiles of K and V.  Rings: Q tiles and dO tiles.  Scores are transposed (lane = key),
 // so that P^T and dS^T are A operands in tensor memory and Q and dO are read with their rows as the
 // contraction.  Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK: 128 columns each.
 // The tensor core runs dV += P^T dO and the next S^T while the warps make dS^T, and dK += dS^T Q and
@@ -181,19 +192,19 @@ __device__ __forceinline__ TileRange query_tiles(const AttnKeyItem& it, int tok)
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_keys_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int pairs) {
-  extern __shared__ uint8_t raw[];
+                     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const RingSizes ring) {
+  extern __shared__ __align__(1024) uint8_t raw[];
   __shared__ BwdShared sh;
-  const uint32_t tiles = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t tiles = smem_u32(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim, tok = a.l.tok;
   const int nb = (d + kColBlock - 1) / kColBlock;
   const uint32_t tile_bytes = (uint32_t)nb * kColBlockBytes;
-  const uint32_t ring = tiles + 2 * tile_bytes;
+  const uint32_t ring_a = tiles + 2 * tile_bytes, ring_b = ring_a + ring.a * tile_bytes;
   volatile int* abort_flag = &sh.abort;
   bwd_init(sh);
   // ring rows that no load writes (a group that does not divide 128)
-  if (tok * g < kAttnRows && warp < 2 * pairs) zero_tile_rows(ring + (uint32_t)warp * tile_bytes, nb, tok * g);
+  if (tok * g < kAttnRows && warp < (int)(ring.a + ring.b)) zero_tile_rows(ring_a + (uint32_t)warp * tile_bytes, nb, tok * g);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
@@ -223,16 +234,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ok = false;
           break;
         }
-        pos = pos.next((uint32_t)pairs);
+        pos = pos.next(kRowSlots);
         tc_fence_after();
         uint32_t s[64], pk[32];
         load_scores(st_col + c0, s);
         const int t = tr.t0 + q * tok;
-        // every row of the tile is there and sees every key
+        // every row of the tile is there and sees every key; else this key is seen by the columns
+        // [from, to) of its half: token t + column / g sees it when key <= token + off
         const bool whole = t + tok <= it.qn && it.off >= it.kn - 1 - t;
+        const int from = max(0, key - it.off - t) * g - 64 * half, to = min(tok, it.qn - t) * g - 64 * half;
         const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sh.nlse2[stg] + 64 * half);
         const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sh.ndelta[stg] + 64 * half);
-        const int4* lk = reinterpret_cast<const int4*>(sh.last_key[stg] + 64 * half);
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {
           const ulonglong2 v = nl[e >> 2];
@@ -244,13 +256,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!whole) {
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const int4 last = lk[e >> 2];
-            s[e] = key > last.x ? 0u : s[e];
-            s[e + 1] = key > last.y ? 0u : s[e + 1];
-            s[e + 2] = key > last.z ? 0u : s[e + 2];
-            s[e + 3] = key > last.w ? 0u : s[e + 3];
-          }
+          for (int e = 0; e < 64; ++e) s[e] = e < from || e >= to ? 0u : s[e];
         }
 #pragma unroll
         for (int e = 0; e < 64; e += 2) pk[e >> 1] = pack2<T>(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
@@ -281,13 +287,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
           if (!whole) {      // a hidden pair counts nothing, whatever dP holds there
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const int4 last = lk[8 * c + (e >> 2)];
-              dp[e] = key > last.x ? 0u : dp[e];
-              dp[e + 1] = key > last.y ? 0u : dp[e + 1];
-              dp[e + 2] = key > last.z ? 0u : dp[e + 2];
-              dp[e + 3] = key > last.w ? 0u : dp[e + 3];
-            }
+            for (int e = 0; e < 32; ++e) dp[e] = 32 * c + e < from || 32 * c + e >= to ? 0u : dp[e];
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) pk[16 * c + (e >> 1)] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
@@ -296,7 +296,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.ds_full));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh.ds_full));
+          mbar_arrive(smem_u32(&sh.row_empty[stg]));
+        }
       }
       if (!ok) break;
       if (tr.n > 0) {
@@ -315,14 +318,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 8) {
     if (lane == 0) {
-      uint32_t n = 0, np = 0;
-      const uint32_t stages = 2u * (uint32_t)pairs, q_bytes = (uint32_t)(nb * tok * g) * 128u;
-      auto load = [&](const CUtensorMap* map, int head, int row) {
-        const uint32_t st = n % stages;
-        if (!mbar_wait(smem_u32(&sh.empty[st]), ((n / stages) & 1u) ^ 1u, abort_flag, kAttnWaitNs)) return false;
-        mbar_arrive_expect_tx(smem_u32(&sh.full[st]), q_bytes);
-        load_tile(ring + st * tile_bytes, map, smem_u32(&sh.full[st]), nb, head, row);
-        ++n;
+      uint32_t la = 0, lb = 0, np = 0;      // loads into the rings and the resident tiles
+      RingPos pa, pb;
+      const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
+      auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t base, RingPos& p, uint32_t slots,
+                      uint32_t& count, int head, int row) {
+        if (!mbar_wait(smem_u32(&empty[p.i]), p.parity ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        mbar_arrive_expect_tx(smem_u32(&full[p.i]), q_bytes);
+        load_tile(base + p.i * tile_bytes, map, smem_u32(&full[p.i]), nb, head, row);
+        p = p.next(slots);
+        ++count;
         return true;
       };
       for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
@@ -339,32 +344,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         load_tile(tiles + tile_bytes, &map_v, smem_u32(&sh.kv_full), nb, kh, it.k0);
         ++np;
         for (int q = 0; ok && q < tr.n; ++q) {
-          ok = load(&map_q, kh * g, it.q0 + tr.t0 + q * tok);
-          if (ok) ok = load(&map_do, kh * g, it.q0 + tr.t0 + q * tok);
+          const int row = it.q0 + tr.t0 + q * tok;
+          ok = load(&map_q, sh.a_full, sh.a_empty, ring_a, pa, ring.a, la, kh * g, row) &&
+               load(&map_do, sh.b_full, sh.b_empty, ring_b, pb, ring.b, lb, kh * g, row);
         }
       }
-      if (*abort_flag) drain_loads(sh, n, stages, np);
+      if (*abort_flag) {
+        drain_loads(&sh.kv_full, np, 1);
+        drain_loads(sh.a_full, la, ring.a);
+        drain_loads(sh.b_full, lb, ring.b);
+      }
     }
     __syncwarp();
   } else if (warp == 9) {
     const uint32_t id_s = idesc_16<T>(128, 128, false), id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
     const int ksteps = (d + 15) / 16;
-    const uint32_t npairs = (uint32_t)pairs;
-    const uint64_t tile_step = (uint64_t)(tile_bytes >> 4), pair_step = 2 * tile_step;
+    const uint64_t tile_step = (uint64_t)(tile_bytes >> 4);
     const uint64_t k_desc = sw128_desc(tiles), v_desc = k_desc + tile_step;
-    const uint64_t q_cols = sw128_desc(ring), do_cols = q_cols + tile_step;               // contraction: columns
-    const uint64_t q_rows = sw128_desc_rows(ring), do_rows = q_rows + tile_step;          // contraction: rows
+    const uint64_t q_cols = sw128_desc(ring_a), do_cols = sw128_desc(ring_b);             // contraction: columns
+    const uint64_t q_rows = sw128_desc_rows(ring_a), do_rows = sw128_desc_rows(ring_b);   // contraction: rows
     uint32_t i = 0, np = 0;
-    RingPos pos;
+    RingPos pa, pb;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
       return ok;
     };
-    // tile `which` (0: Q, 1: dO) of a pair has landed; rows past the sequence's end are zeroed (they
-    // belong to others, and 0 * NaN is NaN)
-    auto wait_tile = [&](const RingPos& p, uint32_t which, int have) {
-      if (!wait(&sh.full[2 * p.i + which], p.parity)) return false;
-      if (have < tok) zero_tile_rows(ring + (2 * p.i + which) * tile_bytes, nb, have * g);
+    // the tile has landed; rows past the sequence's end are zeroed (they belong to others, and 0 * NaN
+    // is NaN)
+    auto wait_tile = [&](uint64_t* full, uint32_t base, const RingPos& p, int have) {
+      if (!wait(&full[p.i], p.parity)) return false;
+      if (have < tok) zero_tile_rows(base + p.i * tile_bytes, nb, have * g);
       return true;
     };
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
@@ -372,42 +381,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const TileRange tr = query_tiles(it, tok);
       const int n = uniform(tr.n), rows0 = uniform(it.qn - tr.t0);     // tokens from the first tile on
       if (n == 0) continue;
-      if (!wait(&sh.kv_full, np++ & 1u) || !wait_tile(pos, 0, rows0)) break;
+      if (!wait(&sh.kv_full, np++ & 1u) || !wait_tile(sh.a_full, ring_a, pa, rows0)) break;
       if (elect_one()) {
-        issue_scores(st_col, k_desc, q_cols + pos.i * pair_step, id_s, ksteps);
+        issue_scores(st_col, k_desc, q_cols + pa.i * tile_step, id_s, ksteps);
         umma_commit(smem_u32(&sh.s_full[0]));
       }
       __syncwarp();
-      if (!wait_tile(pos, 1, rows0)) break;
+      if (!wait_tile(sh.b_full, ring_b, pb, rows0)) break;
       if (elect_one()) {
-        issue_scores(dpt_col, v_desc, do_cols + pos.i * pair_step, id_s, ksteps);
+        issue_scores(dpt_col, v_desc, do_cols + pb.i * tile_step, id_s, ksteps);
         umma_commit(smem_u32(&sh.dp_full));
       }
       __syncwarp();
       for (int q = 0; q < n; ++q, ++i) {
         const bool more = q + 1 < n;
         const int have = rows0 - (q + 1) * tok;
-        const RingPos nx = pos.next(npairs);
-        if (more && !wait_tile(nx, 0, have)) break;
+        const RingPos na = pa.next(ring.a), nbp = pb.next(ring.b);
+        if (more && !wait_tile(sh.a_full, ring_a, na, have)) break;
         if (!wait(&sh.p_full, i & 1u)) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_sum(dv_col, st_col, 32, do_rows + pos.i * pair_step, id_acc, q > 0);             // dV += P^T dO
+          issue_sum(dv_col, st_col, 32, do_rows + pb.i * tile_step, id_acc, q > 0);             // dV += P^T dO
+          umma_commit(smem_u32(&sh.b_empty[pb.i]));
           if (more) {
-            issue_scores(st_col, k_desc, q_cols + nx.i * pair_step, id_s, ksteps);
+            issue_scores(st_col, k_desc, q_cols + na.i * tile_step, id_s, ksteps);
             umma_commit(smem_u32(&sh.s_full[0]));
           }
         }
         __syncwarp();
-        if (more && !wait_tile(nx, 1, have)) break;
+        if (more && !wait_tile(sh.b_full, ring_b, nbp, have)) break;
         if (!wait(&sh.ds_full, i & 1u)) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_sum(dk_col, dpt_col, 32, q_rows + pos.i * pair_step, id_acc, q > 0);             // dK += dS^T Q
-          umma_commit(smem_u32(&sh.empty[2 * pos.i]));
-          umma_commit(smem_u32(&sh.empty[2 * pos.i + 1]));
+          issue_sum(dk_col, dpt_col, 32, q_rows + pa.i * tile_step, id_acc, q > 0);             // dK += dS^T Q
+          umma_commit(smem_u32(&sh.a_empty[pa.i]));
           if (more) {
-            issue_scores(dpt_col, v_desc, do_cols + nx.i * pair_step, id_s, ksteps);
+            issue_scores(dpt_col, v_desc, do_cols + nbp.i * tile_step, id_s, ksteps);
             umma_commit(smem_u32(&sh.dp_full));
           } else {
             umma_commit(smem_u32(&sh.acc_full));
@@ -415,7 +424,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
         __syncwarp();
-        pos = nx;
+        pa = na;
+        pb = nbp;
       }
     }
     if (!ok) drain_mma(sh);
@@ -429,25 +439,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const TileRange tr = query_tiles(it, tok);
       for (int q = 0; q < tr.n; ++q) {
         const uint32_t stg = pos.i;
-        // free when the matrix instructions on the same pair are done
-        if (!mbar_wait_warp<false>(smem_u32(&sh.empty[2 * stg + 1]), pos.parity ^ 1u, abort_flag, kAttnWaitNs)) {
+        if (!mbar_wait_warp<false>(smem_u32(&sh.row_empty[stg]), pos.parity ^ 1u, abort_flag, kAttnWaitNs)) {
           ok = false;
           break;
         }
-        pos = pos.next((uint32_t)pairs);
+        pos = pos.next(kRowSlots);
         const int t = tr.t0 + q * tok;
 #pragma unroll
         for (int c = 0; c < kAttnRows; c += 32) {
           const int x = c + lane, tt = t + x / g;
           RowValue v{-INFINITY, 0.f};
-          int last = -1;
-          if (x < tok * g && tt < it.qn) {
-            v = rows[((int64_t)it.q0 + tt) * a.s.heads_q + kh * g + x % g];
-            last = tt + it.off;
-          }
+          if (x < tok * g && tt < it.qn) v = rows[((int64_t)it.q0 + tt) * a.s.heads_q + kh * g + x % g];
           sh.nlse2[stg][x] = v.nlse2;
           sh.ndelta[stg][x] = v.ndelta;
-          sh.last_key[stg][x] = last;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.row_full[stg]));
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// dq.  Resident: the tiles of Q and dO.  Ring: K and V blocks, alternating.  Lane = query row; the two
+// dq.  Resident: the tiles of Q and dO.  Rings: K blocks and V blocks.  Lane = query row; the two
 // halves of the score warps take 64 keys each.  Tensor memory: S (two buffers; dS over the one it
 // came from), dP, dQ.
 // ---------------------------------------------------------------------------
@@ -475,17 +479,16 @@ __device__ __forceinline__ int key_blocks(const AttnItem& it, int t, int tok, bo
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_queries_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int pairs) {
-  extern __shared__ uint8_t raw[];
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const RingSizes ring) {
+  extern __shared__ __align__(1024) uint8_t raw[];
   __shared__ BwdShared sh;
-  const uint32_t tiles = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t tiles = smem_u32(raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim, tok = a.l.tok;
   const bool causal = a.s.causal != 0;
   const int nb = (d + kColBlock - 1) / kColBlock;
   const uint32_t tile_bytes = (uint32_t)nb * kColBlockBytes;
-  const uint32_t ring = tiles + 2 * tile_bytes;
-  const uint32_t stages = 2u * (uint32_t)pairs;
+  const uint32_t ring_a = tiles + 2 * tile_bytes, ring_b = ring_a + ring.a * tile_bytes;
   volatile int* abort_flag = &sh.abort;
   bwd_init(sh);
   __syncthreads();
@@ -581,14 +584,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == 8) {
     if (lane == 0) {
-      uint32_t n = 0, np = 0;
+      uint32_t la = 0, lb = 0, np = 0;      // loads into the rings and the resident tiles
+      RingPos pa, pb;
       const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
-      auto load = [&](const CUtensorMap* map, int head, int rowk) {
-        const uint32_t st = n % stages;
-        if (!mbar_wait(smem_u32(&sh.empty[st]), ((n / stages) & 1u) ^ 1u, abort_flag, kAttnWaitNs)) return false;
-        mbar_arrive_expect_tx(smem_u32(&sh.full[st]), tile_bytes);
-        load_tile(ring + st * tile_bytes, map, smem_u32(&sh.full[st]), nb, head, rowk);
-        ++n;
+      auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t base, RingPos& p, uint32_t slots,
+                      uint32_t& count, int head, int key) {
+        if (!mbar_wait(smem_u32(&empty[p.i]), p.parity ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        mbar_arrive_expect_tx(smem_u32(&full[p.i]), tile_bytes);
+        load_tile(base + p.i * tile_bytes, map, smem_u32(&full[p.i]), nb, head, key);
+        p = p.next(slots);
+        ++count;
         return true;
       };
       for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
@@ -605,32 +610,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         load_tile(tiles + tile_bytes, &map_do, smem_u32(&sh.kv_full), nb, kh * g, it.q0 + t * tok);
         ++np;
         for (int j = 0; ok && j < nk; ++j) {
-          ok = load(&map_k, kh, it.k0 + j * kAttnKeys);
-          if (ok) ok = load(&map_v, kh, it.k0 + j * kAttnKeys);
+          const int key = it.k0 + j * kAttnKeys;
+          ok = load(&map_k, sh.a_full, sh.a_empty, ring_a, pa, ring.a, la, kh, key) &&
+               load(&map_v, sh.b_full, sh.b_empty, ring_b, pb, ring.b, lb, kh, key);
         }
       }
-      if (*abort_flag) drain_loads(sh, n, stages, np);
+      if (*abort_flag) {
+        drain_loads(&sh.kv_full, np, 1);
+        drain_loads(sh.a_full, la, ring.a);
+        drain_loads(sh.b_full, lb, ring.b);
+      }
     }
     __syncwarp();
   } else if (warp == 9) {
     const uint32_t id_s = idesc_16<T>(128, 128, false), id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
     const int ksteps = (d + 15) / 16;
-    const uint32_t npairs = (uint32_t)pairs;
-    const uint64_t tile_step = (uint64_t)(tile_bytes >> 4), pair_step = 2 * tile_step;
+    const uint64_t tile_step = (uint64_t)(tile_bytes >> 4);
     const uint64_t q_desc = sw128_desc(tiles), do_desc = q_desc + tile_step;
-    const uint64_t k_cols = sw128_desc(ring), v_cols = k_cols + tile_step, k_rows = sw128_desc_rows(ring);
+    const uint64_t k_cols = sw128_desc(ring_a), v_cols = sw128_desc(ring_b), k_rows = sw128_desc_rows(ring_a);
     uint32_t i = 0, np = 0;
-    RingPos pos;
+    RingPos pa, pb;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
       return ok;
     };
     // S of the block at p into buffer b; K rows past the sequence's end are zeroed for dQ += dS K
     auto s_of = [&](const RingPos& p, uint32_t b, int have) {
-      if (!wait(&sh.full[2 * p.i], p.parity)) return false;
-      if (have < kAttnKeys) zero_tile_rows(ring + 2 * p.i * tile_bytes, nb, have);
+      if (!wait(&sh.a_full[p.i], p.parity)) return false;
+      if (have < kAttnKeys) zero_tile_rows(ring_a + p.i * tile_bytes, nb, have);
       if (elect_one()) {
-        issue_scores(tmem + b * 128u, q_desc, k_cols + p.i * pair_step, id_s, ksteps);
+        issue_scores(tmem + b * 128u, q_desc, k_cols + p.i * tile_step, id_s, ksteps);
         umma_commit(smem_u32(&sh.s_full[b]));
       }
       __syncwarp();
@@ -640,34 +649,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const AttnItem it = items[w / (2 * hk)];
       const int n = uniform(key_blocks(it, w & 1, tok, causal)), keys = uniform(it.kn);
       if (n == 0) continue;
-      if (!wait(&sh.kv_full, np++ & 1u) || !s_of(pos, i & 1u, keys) || !wait(&sh.full[2 * pos.i + 1], pos.parity)) break;
+      if (!wait(&sh.kv_full, np++ & 1u) || !s_of(pa, i & 1u, keys) || !wait(&sh.b_full[pb.i], pb.parity)) break;
       if (elect_one()) {
-        issue_scores(dp_col, do_desc, v_cols + pos.i * pair_step, id_s, ksteps);
+        issue_scores(dp_col, do_desc, v_cols + pb.i * tile_step, id_s, ksteps);
         umma_commit(smem_u32(&sh.dp_full));
-        umma_commit(smem_u32(&sh.empty[2 * pos.i + 1]));
+        umma_commit(smem_u32(&sh.b_empty[pb.i]));
       }
       __syncwarp();
       for (int j = 0; j < n; ++j, ++i) {
         const bool more = j + 1 < n;
-        const RingPos nx = pos.next(npairs);
-        if (more && (!s_of(nx, (i + 1) & 1u, keys - (j + 1) * kAttnKeys) || !wait(&sh.full[2 * nx.i + 1], nx.parity))) break;
+        const RingPos na = pa.next(ring.a), nbp = pb.next(ring.b);
+        if (more && (!s_of(na, (i + 1) & 1u, keys - (j + 1) * kAttnKeys) || !wait(&sh.b_full[nbp.i], nbp.parity))) break;
         if (!wait(&sh.ds_full, i & 1u)) break;
         tc_fence_after();
         if (elect_one()) {
           if (more) {
-            issue_scores(dp_col, do_desc, v_cols + nx.i * pair_step, id_s, ksteps);
+            issue_scores(dp_col, do_desc, v_cols + nbp.i * tile_step, id_s, ksteps);
             umma_commit(smem_u32(&sh.dp_full));
-            umma_commit(smem_u32(&sh.empty[2 * nx.i + 1]));
+            umma_commit(smem_u32(&sh.b_empty[nbp.i]));
           }
-          issue_sum(dq_col, tmem + (i & 1u) * 128u, 32, k_rows + pos.i * pair_step, id_acc, j > 0);    // dQ += dS K
-          umma_commit(smem_u32(&sh.empty[2 * pos.i]));
+          issue_sum(dq_col, tmem + (i & 1u) * 128u, 32, k_rows + pa.i * tile_step, id_acc, j > 0);     // dQ += dS K
+          umma_commit(smem_u32(&sh.a_empty[pa.i]));
           if (!more) {
             umma_commit(smem_u32(&sh.acc_full));
             umma_commit(smem_u32(&sh.kv_empty));
           }
         }
         __syncwarp();
-        pos = nx;
+        pa = na;
+        pb = nbp;
       }
     }
     if (!ok) drain_mma(sh);
@@ -685,9 +695,11 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   const int64_t blocks = (s.rows_q * s.heads_q + 15) / 16;
   attn_rows_kernel<T><<<(unsigned)(blocks < 1 ? 1 : blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(a);
   const int tile = (s.head_dim + kColBlock - 1) / kColBlock * kColBlockBytes;
-  int pairs = (kSmemMax - 1024 - (int)sizeof(BwdShared) - 2 * tile) / (2 * tile);
-  if (pairs > kMaxPairs) pairs = kMaxPairs;
-  const int smem = (2 + 2 * pairs) * tile + 1024;
+  const uint32_t slots = (uint32_t)((kSmemMax - 3072) / tile - 2);
+  RingSizes ring;
+  ring.a = slots / 2 + (slots & 1u) < (uint32_t)kMaxSlots ? slots / 2 + (slots & 1u) : (uint32_t)kMaxSlots;
+  ring.b = slots - ring.a < (uint32_t)kMaxSlots ? slots - ring.a : (uint32_t)kMaxSlots;
+  const int smem = (2 + (int)(ring.a + ring.b)) * tile;
   CUtensorMap mq, md, mk, mv;
   if (s.rows_q > 0 && s.rows_k > 0) {
     if (!make_head_map(&mq, a.q, s.dtype, s.head_dim, s.heads_q, s.rows_q, a.q_stride, a.l.group, a.l.tok) ||
@@ -704,15 +716,14 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   }
   const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * 2;
   if (s.rows_k > 0) {
-    e = allow_smem(reinterpret_cast<const void*>(attn_keys_kernel<T>), kSmemMax - (int)sizeof(BwdShared), allowed_keys);
+    e = allow_smem(reinterpret_cast<const void*>(attn_keys_kernel<T>), kSmemMax - 3072, allowed_keys);
     if (e != cudaSuccess) return e;
-    attn_keys_kernel<T><<<(unsigned)(wk < sms ? wk : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, pairs);
+    attn_keys_kernel<T><<<(unsigned)(wk < sms ? wk : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, ring);
   }
   if (s.rows_q > 0) {
-    e = allow_smem(reinterpret_cast<const void*>(attn_queries_kernel<T>), kSmemMax - (int)sizeof(BwdShared),
-                   allowed_queries);
+    e = allow_smem(reinterpret_cast<const void*>(attn_queries_kernel<T>), kSmemMax - 3072, allowed_queries);
     if (e != cudaSuccess) return e;
-    attn_queries_kernel<T><<<(unsigned)(wq < sms ? wq : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, pairs);
+    attn_queries_kernel<T><<<(unsigned)(wq < sms ? wq : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, ring);
   }
   return cudaGetLastError();
 }
