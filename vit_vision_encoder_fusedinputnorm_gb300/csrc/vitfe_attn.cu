@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     };
     auto output = [&](int t, uint32_t st, bool first, uint64_t* also, uint64_t* release) {      // O_t (+)= P_t V
       if (elect_one()) {
-        issue_sum(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u, 0, v_desc + st * tile_step, id_o, !first);
+        issue_sum<128>(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u, v_desc + st * tile_step, id_o, !first);
         if (also) umma_commit(smem_u32(also));
         if (release) umma_commit(smem_u32(release));
       }

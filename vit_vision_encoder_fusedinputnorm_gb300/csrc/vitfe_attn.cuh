@@ -223,13 +223,15 @@ __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint64_t ad, uint6
     if (k < ksteps) umma_bf16(d_tmem, ad + o, bd + o, idesc, k > 0);
   }
 }
-// O, dV, dK or dQ: D (+)= A B, A (128 x 128, 16-bit) in tensor memory, where the second 64 of its
-// contraction start `gap` columns after the first 64's 32, B read by rows.
-__device__ __forceinline__ void issue_sum(uint32_t d_tmem, uint32_t a_tmem, uint32_t gap, uint64_t bd, uint32_t idesc,
+// O, dV, dK or dQ: D (+)= A B, A (128 x 128, 16-bit) in tensor memory, B read by rows.  A was written
+// over fp32 scores by warps of `kPart` columns each, packed at the start of their own columns.
+template <int kPart>
+__device__ __forceinline__ void issue_sum(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd, uint32_t idesc,
                                           uint32_t accumulate) {
 #pragma unroll
   for (int k = 0; k < kAttnKeys / 16; ++k)
-    umma_ta(d_tmem, a_tmem + 8u * k + (k < 4 ? 0u : gap), bd + (uint64_t)(128 * k), idesc, k > 0 ? 1u : accumulate);
+    umma_ta(d_tmem, a_tmem + (uint32_t)(k * 16 / kPart * kPart + k * 16 % kPart / 2), bd + (uint64_t)(128 * k), idesc,
+            k > 0 ? 1u : accumulate);
 }
 
 // mbar_wait_warp<false> all inline: a kernel that shares out its registers anew can hold no call.

@@ -9,7 +9,12 @@
 namespace vitfe {
 namespace {
 
-constexpr int kBwdThreads = 384;     // 8 warps on scores, then loads, matrix instructions, row values, idle
+// Warps of both kernels: 16 on scores (four to a row of the score tile, 32 columns each: their passes
+// are latency, and a scheduler with four of them at hand hides more of it than with two), one on
+// loads, two on matrix instructions (one is held up whenever it has filled the tensor core's short
+// queue; the other one's waits then cost nothing), one that lays out row values and cleans tiles.
+constexpr int kScoreWarps = 16, kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kBwdThreads = 32 * 20;
 constexpr int kMaxSlots = 4;         // of each ring
 constexpr int kRowSlots = 2;         // of the row values
 constexpr int kSmemMax = 227 * 1024;
@@ -60,8 +65,9 @@ struct RingSizes {
 struct BwdShared {
   uint64_t kv_full, kv_empty;                         // the resident pair of tiles
   uint64_t a_full[kMaxSlots], a_empty[kMaxSlots], b_full[kMaxSlots], b_empty[kMaxSlots];
+  uint64_t a_landed[kMaxSlots], b_landed[kMaxSlots];  // of tiles that are cleaned before they are full
   uint64_t row_full[kRowSlots], row_empty[kRowSlots];
-  uint64_t s_full[2], dp_full, p_full, ds_full, acc_full, drain;
+  uint64_t s_full[2], s_empty[2], dp_full, p_full, ds_full, acc_full, drain[2];
   uint32_t tmem;
   int abort;
   alignas(16) float nlse2[kRowSlots][kAttnRows], ndelta[kRowSlots][kAttnRows];   // of a query tile's rows
@@ -74,31 +80,36 @@ __device__ __forceinline__ int deal(int round) {
 }
 __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b); }
 
-__device__ __forceinline__ void bwd_init(BwdShared& sh) {
+// The counts of matrix warps that read the resident tiles and ring B, and that finish an item.
+__device__ __forceinline__ void bwd_init(BwdShared& sh, uint32_t kv_users, uint32_t b_users, uint32_t acc_users) {
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&sh.kv_full), 1);
-    mbar_init(smem_u32(&sh.kv_empty), 1);
+    mbar_init(smem_u32(&sh.kv_empty), kv_users);
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(smem_u32(&sh.a_full[i]), 1);
       mbar_init(smem_u32(&sh.a_empty[i]), 1);
       mbar_init(smem_u32(&sh.b_full[i]), 1);
-      mbar_init(smem_u32(&sh.b_empty[i]), 1);
+      mbar_init(smem_u32(&sh.b_empty[i]), b_users);
+      mbar_init(smem_u32(&sh.a_landed[i]), 1);
+      mbar_init(smem_u32(&sh.b_landed[i]), 1);
     }
     for (int i = 0; i < kRowSlots; ++i) {
       mbar_init(smem_u32(&sh.row_full[i]), 1);
-      mbar_init(smem_u32(&sh.row_empty[i]), 8);
+      mbar_init(smem_u32(&sh.row_empty[i]), kScoreWarps);
     }
-    mbar_init(smem_u32(&sh.s_full[0]), 1);
-    mbar_init(smem_u32(&sh.s_full[1]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.s_empty[i]), 1);
+      mbar_init(smem_u32(&sh.drain[i]), 1);
+    }
     mbar_init(smem_u32(&sh.dp_full), 1);
-    mbar_init(smem_u32(&sh.p_full), 8);
-    mbar_init(smem_u32(&sh.ds_full), 8);
-    mbar_init(smem_u32(&sh.acc_full), 1);
-    mbar_init(smem_u32(&sh.drain), 1);
+    mbar_init(smem_u32(&sh.p_full), kScoreWarps);
+    mbar_init(smem_u32(&sh.ds_full), kScoreWarps);
+    mbar_init(smem_u32(&sh.acc_full), acc_users);
     sh.abort = 0;
     fence_mbar_init();
   }
-  if ((threadIdx.x >> 5) == 9) {
+  if ((threadIdx.x >> 5) == kMmaWarp) {
     tmem_alloc(smem_u32(&sh.tmem), 512);
     tmem_relinquish();
     tc_fence_before();
@@ -108,7 +119,7 @@ __device__ __forceinline__ void bwd_init(BwdShared& sh) {
 __device__ __forceinline__ void bwd_end(BwdShared& sh, uint32_t tmem, int32_t* status) {
   tc_fence_before();
   __syncthreads();
-  if ((threadIdx.x >> 5) == 9) {
+  if ((threadIdx.x >> 5) == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -119,19 +130,19 @@ __device__ __forceinline__ void bwd_end(BwdShared& sh, uint32_t tmem, int32_t* s
 }
 
 // After an abort: the loads of one ring, or of the resident tiles, land on their own; wait for the last
-// `n` uses of the slots at `full` before the CTA ends.
+// `n` uses of the slots at `full` before the CTA ends (2 ms: a tile to be cleaned does not get there).
 __device__ __forceinline__ void drain_loads(uint64_t* full, uint32_t n, uint32_t slots) {
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = n - (n < slots ? n : slots); i < n; ++i)
-    while (!mbar_try_wait(smem_u32(&full[i % slots]), (i / slots) & 1u) && global_timer_ns() - t0 < kAttnWaitNs) {
+    while (!mbar_try_wait(smem_u32(&full[i % slots]), (i / slots) & 1u) && global_timer_ns() - t0 < 2000000ull) {
     }
 }
 
-// ... and the matrix instructions in flight.
-__device__ __forceinline__ void drain_mma(BwdShared& sh) {
-  if (elect_one()) umma_commit(smem_u32(&sh.drain));
+// ... and this warp's matrix instructions in flight.
+__device__ __forceinline__ void drain_mma(uint64_t* bar) {
+  if (elect_one()) umma_commit(smem_u32(bar));
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(smem_u32(&sh.drain), 0) && global_timer_ns() - t0 < kAttnWaitNs) {
+  while (!mbar_try_wait(smem_u32(bar), 0) && global_timer_ns() - t0 < kAttnWaitNs) {
   }
   __syncwarp();
 }
@@ -141,13 +152,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
   for (int b = 0; b < nb; ++b) tma_load_3d(dst + (uint32_t)b * kColBlockBytes, map, bar, b * kColBlock, head, row);
 }
 
-// 64 scores of a thread and the 64 values of a row vector, as pairs: the row vector is the same for
-// every lane, so shared memory serves four of its floats to the whole warp at once.
-__device__ __forceinline__ void load_scores(uint32_t col, uint32_t (&s)[64]) {
-  tmem_ld_32x32b_x32(col, *reinterpret_cast<uint32_t(*)[32]>(s));
-  tmem_ld_32x32b_x32(col + 32u, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-  tmem_wait_ld();
-}
 __device__ __forceinline__ uint64_t pair_of(const uint32_t* v) { return (uint64_t)v[0] | ((uint64_t)v[1] << 32); }
 
 // 16-bit rows of an accumulator, columns [c0, c1) in steps of 16, times `f`.
@@ -183,11 +187,10 @@ __device__ __forceinline__ TileRange query_tiles(const AttnKeyItem& it, int tok)
 }
 
 // ---------------------------------------------------------------------------
-// dk, dv.  Resident: the tiles of K and V.  Rings: Q tiles and dO tiles.  Scores are transposed (lane = key),
-// so that P^T and dS^T are A operands in tensor memory and Q and dO are read with their rows as the
+// dk, dv.  Resident: the tiles of K and V.  Rings: Q tiles and dO tiles.  Scores are transposed (lane =
+// key), so that P^T and dS^T are A operands in tensor memory and Q and dO are read with their rows as the
 // contraction.  Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK: 128 columns each.
-// The tensor core runs dV += P^T dO and the next S^T while the warps make dS^T, and dK += dS^T Q and
-// the next dP^T while they make the next P^T.
+// One matrix warp runs dV += P^T dO and the next S^T, the other dK += dS^T Q and the next dP^T.
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tile_bytes = (uint32_t)nb * kColBlockBytes;
   const uint32_t ring_a = tiles + 2 * tile_bytes, ring_b = ring_a + ring.a * tile_bytes;
   volatile int* abort_flag = &sh.abort;
-  bwd_init(sh);
+  bwd_init(sh, 2, 2, 2);
   // ring rows that no load writes (a group that does not divide 128)
   if (tok * g < kAttnRows && warp < (int)(ring.a + ring.b)) zero_tile_rows(ring_a + (uint32_t)warp * tile_bytes, nb, tok * g);
   __syncthreads();
@@ -213,12 +216,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const AttnKeyItem* items = reinterpret_cast<const AttnKeyItem*>(a.plan + a.l.at_keys);
   const int works = hdr->n_keys * hk;
   bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {      // by a whole warp
+    ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
+    return ok;
+  };
 
-  if (warp < 8) {
-    const int half = warp >> 2;
+  if (warp < kScoreWarps) {
+    const int part = warp >> 2;                      // columns [32 part, 32 part + 32)
     const int key = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t c0 = lanes + 64u * half;
+    const uint32_t c0 = lanes + 32u * part;
     const float scale2 = a.scale * kLog2e;
     const uint64_t sc = f32x2(scale2, scale2);
     uint32_t i = 0, acc = 0;                         // tiles so far, finished items (phases)
@@ -229,24 +236,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const TileRange tr = query_tiles(it, tok);
       for (int q = 0; q < tr.n; ++q, ++i) {
         const uint32_t stg = pos.i;
-        if (!mbar_wait_warp<false>(smem_u32(&sh.row_full[stg]), pos.parity, abort_flag, kAttnWaitNs) ||
-            !mbar_wait_warp<false>(smem_u32(&sh.s_full[0]), i & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
+        if (!wait(&sh.row_full[stg], pos.parity) || !wait(&sh.s_full[0], i & 1u)) break;
         pos = pos.next(kRowSlots);
         tc_fence_after();
-        uint32_t s[64], pk[32];
-        load_scores(st_col + c0, s);
+        uint32_t s[32], pk[16];
+        tmem_ld_32x32b_x32(st_col + c0, s);
+        tmem_wait_ld();
         const int t = tr.t0 + q * tok;
         // every row of the tile is there and sees every key; else this key is seen by the columns
-        // [from, to) of its half: token t + column / g sees it when key <= token + off
+        // [from, to) of its part: token t + column / g sees it when key <= token + off
         const bool whole = t + tok <= it.qn && it.off >= it.kn - 1 - t;
-        const int from = max(0, key - it.off - t) * g - 64 * half, to = min(tok, it.qn - t) * g - 64 * half;
-        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sh.nlse2[stg] + 64 * half);
-        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sh.ndelta[stg] + 64 * half);
+        const int from = max(0, key - it.off - t) * g - 32 * part, to = min(tok, it.qn - t) * g - 32 * part;
+        // the row vectors are the same for every lane: shared memory serves four floats to the warp at once
+        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sh.nlse2[stg] + 32 * part);
+        const ulonglong2* nd = reinterpret_cast<const ulonglong2*>(sh.ndelta[stg] + 32 * part);
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
+        for (int e = 0; e < 32; e += 4) {
           const ulonglong2 v = nl[e >> 2];
           const uint64_t x = fma_f32x2(pair_of(s + e), sc, v.x), y = fma_f32x2(pair_of(s + e + 2), sc, v.y);
           s[e] = __float_as_uint(exp2_approx(lo_f32(x)));
@@ -256,43 +261,37 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!whole) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) s[e] = e < from || e >= to ? 0u : s[e];
+          for (int e = 0; e < 32; ++e) s[e] = e < from || e >= to ? 0u : s[e];
         }
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) pk[e >> 1] = pack2<T>(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-        tmem_st_32x32b_x32(st_col + c0, pk);
+        for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack2<T>(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        tmem_st_32x32b_x16(st_col + c0, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.p_full));
-        if (!mbar_wait_warp<false>(smem_u32(&sh.dp_full), i & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
+        if (!wait(&sh.dp_full, i & 1u)) break;
         tc_fence_after();
+        uint32_t dp[32];
+        tmem_ld_32x32b_x32(dpt_col + c0, dp);
+        tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t dp[32];
-          tmem_ld_32x32b_x32(dpt_col + c0 + 32u * c, dp);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 v = nd[8 * c + (e >> 2)];
-            const uint64_t x = mul_f32x2(pair_of(s + 32 * c + e), add_f32x2(pair_of(dp + e), v.x));
-            const uint64_t y = mul_f32x2(pair_of(s + 32 * c + e + 2), add_f32x2(pair_of(dp + e + 2), v.y));
-            dp[e] = (uint32_t)x;
-            dp[e + 1] = (uint32_t)(x >> 32);
-            dp[e + 2] = (uint32_t)y;
-            dp[e + 3] = (uint32_t)(y >> 32);
-          }
-          if (!whole) {      // a hidden pair counts nothing, whatever dP holds there
-#pragma unroll
-            for (int e = 0; e < 32; ++e) dp[e] = 32 * c + e < from || 32 * c + e >= to ? 0u : dp[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) pk[16 * c + (e >> 1)] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 v = nd[e >> 2];
+          const uint64_t x = mul_f32x2(pair_of(s + e), add_f32x2(pair_of(dp + e), v.x));
+          const uint64_t y = mul_f32x2(pair_of(s + e + 2), add_f32x2(pair_of(dp + e + 2), v.y));
+          dp[e] = (uint32_t)x;
+          dp[e + 1] = (uint32_t)(x >> 32);
+          dp[e + 2] = (uint32_t)y;
+          dp[e + 3] = (uint32_t)(y >> 32);
         }
-        tmem_st_32x32b_x32(dpt_col + c0, pk);
+        if (!whole) {      // a hidden pair counts nothing, whatever dP holds there
+#pragma unroll
+          for (int e = 0; e < 32; ++e) dp[e] = e < from || e >= to ? 0u : dp[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+        tmem_st_32x32b_x16(dpt_col + c0, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -301,22 +300,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mbar_arrive(smem_u32(&sh.row_empty[stg]));
         }
       }
-      if (!ok) break;
-      if (tr.n > 0) {
-        if (!mbar_wait_warp<false>(smem_u32(&sh.acc_full), acc & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
-        ++acc;
-        tc_fence_after();
-      }
+      if (!ok || (tr.n > 0 && !wait(&sh.acc_full, acc++ & 1u))) break;
+      tc_fence_after();
+      // parts 0, 1: the halves of dV's columns; 2, 3: of dK's
       const int64_t krow = (int64_t)it.k0 + key;
-      T* out = half == 0 ? static_cast<T*>(a.dv) + krow * a.dv_stride : static_cast<T*>(a.dk) + krow * a.dk_stride;
-      store_rows<T>((half == 0 ? dv_col : dk_col) + lanes, 0, d, d, half == 0 ? 1.f : a.scale, out + kh * d, key < it.kn,
-                    tr.n > 0);
+      const bool is_v = part < 2;
+      const int mid = (d / 2 + 15) / 16 * 16;
+      T* out = is_v ? static_cast<T*>(a.dv) + krow * a.dv_stride : static_cast<T*>(a.dk) + krow * a.dk_stride;
+      store_rows<T>((is_v ? dv_col : dk_col) + lanes, part & 1 ? mid : 0, part & 1 ? d : mid, d, is_v ? 1.f : a.scale,
+                    out + kh * d, key < it.kn, tr.n > 0);
       tc_fence_before();
     }
-  } else if (warp == 8) {
+  } else if (warp == kLoadWarp) {
     if (lane == 0) {
       uint32_t la = 0, lb = 0, np = 0;      // loads into the rings and the resident tiles
       RingPos pa, pb;
@@ -344,9 +339,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         load_tile(tiles + tile_bytes, &map_v, smem_u32(&sh.kv_full), nb, kh, it.k0);
         ++np;
         for (int q = 0; ok && q < tr.n; ++q) {
-          const int row = it.q0 + tr.t0 + q * tok;
-          ok = load(&map_q, sh.a_full, sh.a_empty, ring_a, pa, ring.a, la, kh * g, row) &&
-               load(&map_do, sh.b_full, sh.b_empty, ring_b, pb, ring.b, lb, kh * g, row);
+          const int t = tr.t0 + q * tok;
+          const bool clean = it.qn - t < tok;
+          ok = load(&map_q, clean ? sh.a_landed : sh.a_full, sh.a_empty, ring_a, pa, ring.a, la, kh * g, it.q0 + t) &&
+               load(&map_do, clean ? sh.b_landed : sh.b_full, sh.b_empty, ring_b, pb, ring.b, lb, kh * g, it.q0 + t);
         }
       }
       if (*abort_flag) {
@@ -356,7 +352,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    const bool first = warp == kMmaWarp;             // S^T and dV; the other: dP^T and dK
     const uint32_t id_s = idesc_16<T>(128, 128, false), id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
     const int ksteps = (d + 15) / 16;
     const uint64_t tile_step = (uint64_t)(tile_bytes >> 4);
@@ -365,107 +362,120 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint64_t q_rows = sw128_desc_rows(ring_a), do_rows = sw128_desc_rows(ring_b);   // contraction: rows
     uint32_t i = 0, np = 0;
     RingPos pa, pb;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
-      return ok;
-    };
-    // the tile has landed; rows past the sequence's end are zeroed (they belong to others, and 0 * NaN
-    // is NaN)
-    auto wait_tile = [&](uint64_t* full, uint32_t base, const RingPos& p, int have) {
-      if (!wait(&full[p.i], p.parity)) return false;
-      if (have < tok) zero_tile_rows(base + p.i * tile_bytes, nb, have * g);
-      return true;
-    };
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnKeyItem it = items[w / hk];
-      const TileRange tr = query_tiles(it, tok);
-      const int n = uniform(tr.n), rows0 = uniform(it.qn - tr.t0);     // tokens from the first tile on
+      const int n = uniform(query_tiles(it, tok).n);
       if (n == 0) continue;
-      if (!wait(&sh.kv_full, np++ & 1u) || !wait_tile(sh.a_full, ring_a, pa, rows0)) break;
-      if (elect_one()) {
-        issue_scores(st_col, k_desc, q_cols + pa.i * tile_step, id_s, ksteps);
-        umma_commit(smem_u32(&sh.s_full[0]));
-      }
-      __syncwarp();
-      if (!wait_tile(sh.b_full, ring_b, pb, rows0)) break;
-      if (elect_one()) {
-        issue_scores(dpt_col, v_desc, do_cols + pb.i * tile_step, id_s, ksteps);
-        umma_commit(smem_u32(&sh.dp_full));
+      if (!wait(&sh.kv_full, np++ & 1u)) break;
+      if (first) {
+        if (!wait(&sh.a_full[pa.i], pa.parity)) break;
+        if (elect_one()) {
+          issue_scores(st_col, k_desc, q_cols + pa.i * tile_step, id_s, ksteps);
+          umma_commit(smem_u32(&sh.s_full[0]));
+        }
+      } else {
+        if (!wait(&sh.b_full[pb.i], pb.parity)) break;
+        if (elect_one()) {
+          issue_scores(dpt_col, v_desc, do_cols + pb.i * tile_step, id_s, ksteps);
+          umma_commit(smem_u32(&sh.dp_full));
+          umma_commit(smem_u32(&sh.b_empty[pb.i]));
+        }
       }
       __syncwarp();
       for (int q = 0; q < n; ++q, ++i) {
         const bool more = q + 1 < n;
-        const int have = rows0 - (q + 1) * tok;
         const RingPos na = pa.next(ring.a), nbp = pb.next(ring.b);
-        if (more && !wait_tile(sh.a_full, ring_a, na, have)) break;
-        if (!wait(&sh.p_full, i & 1u)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_sum(dv_col, st_col, 32, do_rows + pb.i * tile_step, id_acc, q > 0);             // dV += P^T dO
-          umma_commit(smem_u32(&sh.b_empty[pb.i]));
-          if (more) {
-            issue_scores(st_col, k_desc, q_cols + na.i * tile_step, id_s, ksteps);
-            umma_commit(smem_u32(&sh.s_full[0]));
+        if (first) {
+          if (!wait(&sh.b_full[pb.i], pb.parity) || (more && !wait(&sh.a_full[na.i], na.parity)) ||
+              !wait(&sh.p_full, i & 1u))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_sum<32>(dv_col, st_col, do_rows + pb.i * tile_step, id_acc, q > 0);
+            umma_commit(smem_u32(&sh.b_empty[pb.i]));
+            if (more) {
+              issue_scores(st_col, k_desc, q_cols + na.i * tile_step, id_s, ksteps);
+              umma_commit(smem_u32(&sh.s_full[0]));
+            }
+          }
+        } else {
+          if (!wait(&sh.a_full[pa.i], pa.parity) || (more && !wait(&sh.b_full[nbp.i], nbp.parity)) ||
+              !wait(&sh.ds_full, i & 1u))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_sum<32>(dk_col, dpt_col, q_rows + pa.i * tile_step, id_acc, q > 0);
+            umma_commit(smem_u32(&sh.a_empty[pa.i]));      // (S^T of this tile was done before its dS^T)
+            if (more) {
+              issue_scores(dpt_col, v_desc, do_cols + nbp.i * tile_step, id_s, ksteps);
+              umma_commit(smem_u32(&sh.dp_full));
+              umma_commit(smem_u32(&sh.b_empty[nbp.i]));
+            }
           }
         }
         __syncwarp();
-        if (more && !wait_tile(sh.b_full, ring_b, nbp, have)) break;
-        if (!wait(&sh.ds_full, i & 1u)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_sum(dk_col, dpt_col, 32, q_rows + pa.i * tile_step, id_acc, q > 0);             // dK += dS^T Q
-          umma_commit(smem_u32(&sh.a_empty[pa.i]));
-          if (more) {
-            issue_scores(dpt_col, v_desc, do_cols + nbp.i * tile_step, id_s, ksteps);
-            umma_commit(smem_u32(&sh.dp_full));
-          } else {
-            umma_commit(smem_u32(&sh.acc_full));
-            umma_commit(smem_u32(&sh.kv_empty));
-          }
+        if (!more && elect_one()) {
+          umma_commit(smem_u32(&sh.acc_full));
+          umma_commit(smem_u32(&sh.kv_empty));
         }
         __syncwarp();
         pa = na;
         pb = nbp;
       }
     }
-    if (!ok) drain_mma(sh);
-  } else if (warp == 10) {
-    // each query tile's row values beside it
+    if (!ok) drain_mma(&sh.drain[first ? 0 : 1]);
+  } else {
+    // each query tile's row values beside it; and tiles that reach past their sequence: rows of others
+    // are zeroed (their P and dS are 0, but 0 * NaN is NaN)
     const RowValue* rows = static_cast<const RowValue*>(a.workspace);
     RingPos pos;
+    uint32_t seen = 0, pa = 0, pb = 0;             // tiles so far; a parity bit for each slot's cleaned uses
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnKeyItem it = items[w / hk];
       const int kh = w % hk;
       const TileRange tr = query_tiles(it, tok);
       for (int q = 0; q < tr.n; ++q) {
         const uint32_t stg = pos.i;
-        if (!mbar_wait_warp<false>(smem_u32(&sh.row_empty[stg]), pos.parity ^ 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
-        pos = pos.next(kRowSlots);
         const int t = tr.t0 + q * tok;
+        RowValue v[kAttnRows / 32];
 #pragma unroll
-        for (int c = 0; c < kAttnRows; c += 32) {
-          const int x = c + lane, tt = t + x / g;
-          RowValue v{-INFINITY, 0.f};
-          if (x < tok * g && tt < it.qn) v = rows[((int64_t)it.q0 + tt) * a.s.heads_q + kh * g + x % g];
-          sh.nlse2[stg][x] = v.nlse2;
-          sh.ndelta[stg][x] = v.ndelta;
+        for (int c = 0; c < kAttnRows / 32; ++c) {
+          const int x = 32 * c + lane, tt = t + x / g;
+          v[c] = RowValue{-INFINITY, 0.f};
+          if (x < tok * g && tt < it.qn) v[c] = rows[((int64_t)it.q0 + tt) * a.s.heads_q + kh * g + x % g];
+        }
+        if (!wait(&sh.row_empty[stg], pos.parity ^ 1u)) break;
+        pos = pos.next(kRowSlots);
+#pragma unroll
+        for (int c = 0; c < kAttnRows / 32; ++c) {
+          sh.nlse2[stg][32 * c + lane] = v[c].nlse2;
+          sh.ndelta[stg][32 * c + lane] = v[c].ndelta;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.row_full[stg]));
       }
-      if (!ok) break;
+      if (!ok || tr.n == 0) continue;
+      seen += (uint32_t)tr.n;
+      const int have = it.qn - tr.t0 - (tr.n - 1) * tok;
+      if (have >= tok) continue;
+      const uint32_t sa = (seen - 1u) % ring.a, sb = (seen - 1u) % ring.b;
+      if (!wait(&sh.a_landed[sa], (pa >> sa) & 1u)) break;
+      pa ^= 1u << sa;
+      zero_tile_rows(ring_a + sa * tile_bytes, nb, have * g);
+      if (lane == 0) mbar_arrive(smem_u32(&sh.a_full[sa]));
+      if (!wait(&sh.b_landed[sb], (pb >> sb) & 1u)) break;
+      pb ^= 1u << sb;
+      zero_tile_rows(ring_b + sb * tile_bytes, nb, have * g);
+      if (lane == 0) mbar_arrive(smem_u32(&sh.b_full[sb]));
     }
   }
   bwd_end(sh, tmem, a.status);
 }
 
 // ---------------------------------------------------------------------------
-// dq.  Resident: the tiles of Q and dO.  Rings: K blocks and V blocks.  Lane = query row; the two
-// halves of the score warps take 64 keys each.  Tensor memory: S (two buffers; dS over the one it
-// came from), dP, dQ.
+// dq.  Resident: the tiles of Q and dO.  Rings: K blocks and V blocks.  Lane = query row; four threads to
+// a row, 32 keys each.  Tensor memory: S (two buffers; dS over the one it came from), dP, dQ.
+// One matrix warp runs S and dP, the other dQ += dS K.
 // ---------------------------------------------------------------------------
 // Key blocks that tile t of an item reads, over the item's whole range (of a cut item the first
 // piece takes all of it: enough rows to fill the GPU are the rule in training).
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tile_bytes = (uint32_t)nb * kColBlockBytes;
   const uint32_t ring_a = tiles + 2 * tile_bytes, ring_b = ring_a + ring.a * tile_bytes;
   volatile int* abort_flag = &sh.abort;
-  bwd_init(sh);
+  bwd_init(sh, 1, 1, 1);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
@@ -499,9 +509,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
   const int works = hdr->n_items * hk * 2;                      // (item, key head, tile)
   bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {             // by a whole warp
+    ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
+    return ok;
+  };
 
-  if (warp < 8) {
-    const int half = warp >> 2;
+  if (warp < kScoreWarps) {
+    const int part = warp >> 2;                                 // keys [32 part, 32 part + 32) of a block
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float scale2 = a.scale * kLog2e;
@@ -521,68 +535,52 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       else lim = 0;
       const uint64_t nl = f32x2(v.nlse2, v.nlse2), nd = f32x2(v.ndelta, v.ndelta);
       for (int j = 0; j < n; ++j, ++i) {
-        const uint32_t s_col = tmem + lanes + (i & 1u) * 128u + 64u * half;
-        if (!mbar_wait_warp<false>(smem_u32(&sh.s_full[i & 1u]), (i >> 1) & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
+        const uint32_t s_col = tmem + lanes + (i & 1u) * 128u + 32u * part;
+        if (!wait(&sh.s_full[i & 1u], (i >> 1) & 1u)) break;
         tc_fence_after();
-        uint32_t s[64], pk[32];
-        load_scores(s_col, s);
-        const int left = lim - j * kAttnKeys - 64 * half;
-        const bool whole = __all_sync(0xffffffffu, left >= 64);
+        uint32_t s[32], dp[32], pk[16];
+        tmem_ld_32x32b_x32(s_col, s);
+        tmem_wait_ld();
+        const int left = lim - j * kAttnKeys - 32 * part;
+        const bool whole = __all_sync(0xffffffffu, left >= 32);
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
+        for (int e = 0; e < 32; e += 2) {
           const uint64_t x = fma_f32x2(pair_of(s + e), sc, nl);
           s[e] = __float_as_uint(exp2_approx(lo_f32(x)));
           s[e + 1] = __float_as_uint(exp2_approx(hi_f32(x)));
         }
-        if (!mbar_wait_warp<false>(smem_u32(&sh.dp_full), i & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
+        if (!wait(&sh.dp_full, i & 1u)) break;
         tc_fence_after();
+        tmem_ld_32x32b_x32(dp_col + lanes + 32u * part, dp);
+        tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t dp[32];
-          tmem_ld_32x32b_x32(dp_col + lanes + 64u * half + 32u * c, dp);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t x = mul_f32x2(pair_of(s + 32 * c + e), add_f32x2(pair_of(dp + e), nd));
-            dp[e] = (uint32_t)x;
-            dp[e + 1] = (uint32_t)(x >> 32);
-          }
-          if (!whole) {      // a hidden key counts nothing, whatever dP holds there
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= left) dp[e] = 0u;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) pk[16 * c + (e >> 1)] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t x = mul_f32x2(pair_of(s + e), add_f32x2(pair_of(dp + e), nd));
+          dp[e] = (uint32_t)x;
+          dp[e + 1] = (uint32_t)(x >> 32);
         }
-        tmem_st_32x32b_x32(s_col, pk);
+        if (!whole) {      // a hidden key counts nothing, whatever dP holds there
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e >= left) dp[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack2<T>(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+        tmem_st_32x32b_x16(s_col, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.ds_full));
       }
-      if (!ok) break;
-      if (n > 0) {
-        if (!mbar_wait_warp<false>(smem_u32(&sh.acc_full), acc & 1u, abort_flag, kAttnWaitNs)) {
-          ok = false;
-          break;
-        }
-        ++acc;
-        tc_fence_after();
-      }
-      // each half of the warps stores half of the columns
-      const int mid = (d / 2 + 15) / 16 * 16;
+      if (!ok || (n > 0 && !wait(&sh.acc_full, acc++ & 1u))) break;
+      tc_fence_after();
+      // each part of the warps stores a quarter of the columns, in steps of 16
+      const int each = (d + 63) / 64 * 16, c0 = min(d, each * part), c1 = min(d, each * (part + 1));
       T* out = static_cast<T*>(a.dq) + ((int64_t)it.q0 + my_tok) * a.dq_stride + head * d;
-      store_rows<T>(dq_col + lanes, half == 0 ? 0 : mid, half == 0 ? mid : d, d, a.scale, out, live, n > 0);
+      store_rows<T>(dq_col + lanes, c0, c1, d, a.scale, out, live, n > 0);
       tc_fence_before();
     }
-  } else if (warp == 8) {
+  } else if (warp == kLoadWarp) {
     if (lane == 0) {
       uint32_t la = 0, lb = 0, np = 0;      // loads into the rings and the resident tiles
       RingPos pa, pb;
@@ -611,7 +609,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ++np;
         for (int j = 0; ok && j < nk; ++j) {
           const int key = it.k0 + j * kAttnKeys;
-          ok = load(&map_k, sh.a_full, sh.a_empty, ring_a, pa, ring.a, la, kh, key) &&
+          const bool clean = it.kn - j * kAttnKeys < kAttnKeys;
+          ok = load(&map_k, clean ? sh.a_landed : sh.a_full, sh.a_empty, ring_a, pa, ring.a, la, kh, key) &&
                load(&map_v, sh.b_full, sh.b_empty, ring_b, pb, ring.b, lb, kh, key);
         }
       }
@@ -622,7 +621,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    const bool first = warp == kMmaWarp;             // S and dP; the other: dQ
     const uint32_t id_s = idesc_16<T>(128, 128, false), id_acc = idesc_16<T>(128, (d + 15) / 16 * 16, true);
     const int ksteps = (d + 15) / 16;
     const uint64_t tile_step = (uint64_t)(tile_bytes >> 4);
@@ -630,57 +630,81 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint64_t k_cols = sw128_desc(ring_a), v_cols = sw128_desc(ring_b), k_rows = sw128_desc_rows(ring_a);
     uint32_t i = 0, np = 0;
     RingPos pa, pb;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
-      return ok;
-    };
-    // S of the block at p into buffer b; K rows past the sequence's end are zeroed for dQ += dS K
-    auto s_of = [&](const RingPos& p, uint32_t b, int have) {
-      if (!wait(&sh.a_full[p.i], p.parity)) return false;
-      if (have < kAttnKeys) zero_tile_rows(ring_a + p.i * tile_bytes, nb, have);
+    // S of block x into its buffer, when dQ has taken the dS that was there
+    auto s_of = [&](const RingPos& p, uint32_t x) {
+      if (!wait(&sh.a_full[p.i], p.parity) || !wait(&sh.s_empty[x & 1u], ((x >> 1) & 1u) ^ 1u)) return false;
+      tc_fence_after();
       if (elect_one()) {
-        issue_scores(tmem + b * 128u, q_desc, k_cols + p.i * tile_step, id_s, ksteps);
-        umma_commit(smem_u32(&sh.s_full[b]));
+        issue_scores(tmem + (x & 1u) * 128u, q_desc, k_cols + p.i * tile_step, id_s, ksteps);
+        umma_commit(smem_u32(&sh.s_full[x & 1u]));
       }
       __syncwarp();
       return true;
     };
-    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
-      const AttnItem it = items[w / (2 * hk)];
-      const int n = uniform(key_blocks(it, w & 1, tok, causal)), keys = uniform(it.kn);
-      if (n == 0) continue;
-      if (!wait(&sh.kv_full, np++ & 1u) || !s_of(pa, i & 1u, keys) || !wait(&sh.b_full[pb.i], pb.parity)) break;
+    auto dp_of = [&](const RingPos& p) {
       if (elect_one()) {
-        issue_scores(dp_col, do_desc, v_cols + pb.i * tile_step, id_s, ksteps);
+        issue_scores(dp_col, do_desc, v_cols + p.i * tile_step, id_s, ksteps);
         umma_commit(smem_u32(&sh.dp_full));
-        umma_commit(smem_u32(&sh.b_empty[pb.i]));
+        umma_commit(smem_u32(&sh.b_empty[p.i]));
       }
       __syncwarp();
+    };
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnItem it = items[w / (2 * hk)];
+      const int n = uniform(key_blocks(it, w & 1, tok, causal));
+      if (n == 0) continue;
+      if (first) {
+        if (!wait(&sh.kv_full, np++ & 1u) || !s_of(pa, i) || !wait(&sh.b_full[pb.i], pb.parity)) break;
+        dp_of(pb);
+      }
       for (int j = 0; j < n; ++j, ++i) {
         const bool more = j + 1 < n;
         const RingPos na = pa.next(ring.a), nbp = pb.next(ring.b);
-        if (more && (!s_of(na, (i + 1) & 1u, keys - (j + 1) * kAttnKeys) || !wait(&sh.b_full[nbp.i], nbp.parity))) break;
-        if (!wait(&sh.ds_full, i & 1u)) break;
-        tc_fence_after();
-        if (elect_one()) {
+        if (first) {
           if (more) {
-            issue_scores(dp_col, do_desc, v_cols + nbp.i * tile_step, id_s, ksteps);
-            umma_commit(smem_u32(&sh.dp_full));
-            umma_commit(smem_u32(&sh.b_empty[nbp.i]));
+            if (!s_of(na, i + 1) || !wait(&sh.b_full[nbp.i], nbp.parity) || !wait(&sh.ds_full, i & 1u)) break;
+            tc_fence_after();
+            dp_of(nbp);
+          } else {
+            // the next item's first dP waits for the scores of this one's last block, as any other
+            if (elect_one()) umma_commit(smem_u32(&sh.kv_empty));
+            __syncwarp();
+            if (!wait(&sh.ds_full, i & 1u)) break;
+            tc_fence_after();
           }
-          issue_sum(dq_col, tmem + (i & 1u) * 128u, 32, k_rows + pa.i * tile_step, id_acc, j > 0);     // dQ += dS K
-          umma_commit(smem_u32(&sh.a_empty[pa.i]));
-          if (!more) {
-            umma_commit(smem_u32(&sh.acc_full));
-            umma_commit(smem_u32(&sh.kv_empty));
+        } else {
+          if (!wait(&sh.a_full[pa.i], pa.parity) || !wait(&sh.ds_full, i & 1u)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_sum<32>(dq_col, tmem + (i & 1u) * 128u, k_rows + pa.i * tile_step, id_acc, j > 0);
+            umma_commit(smem_u32(&sh.a_empty[pa.i]));      // (S of this block was done before its dS)
+            umma_commit(smem_u32(&sh.s_empty[i & 1u]));
+            if (!more) umma_commit(smem_u32(&sh.acc_full));
           }
+          __syncwarp();
         }
-        __syncwarp();
         pa = na;
         pb = nbp;
       }
     }
-    if (!ok) drain_mma(sh);
+    if (!ok) drain_mma(&sh.drain[first ? 0 : 1]);
+  } else {
+    // K blocks that reach past their sequence: rows of others are zeroed for dQ (their dS is 0, but
+    // 0 * NaN is NaN)
+    uint32_t na = 0, pa = 0;                         // blocks so far; a parity bit for each slot's cleaned uses
+    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      const AttnItem it = items[w / (2 * hk)];
+      const int n = key_blocks(it, w & 1, tok, causal);
+      if (n == 0) continue;
+      na += (uint32_t)n;
+      const int have = it.kn - (n - 1) * kAttnKeys;
+      if (have >= kAttnKeys) continue;
+      const uint32_t sa = (na - 1u) % ring.a;
+      if (!wait(&sh.a_landed[sa], (pa >> sa) & 1u)) break;
+      pa ^= 1u << sa;
+      zero_tile_rows(ring_a + sa * tile_bytes, nb, have);
+      if (lane == 0) mbar_arrive(smem_u32(&sh.a_full[sa]));
+    }
   }
   bwd_end(sh, tmem, a.status);
 }
