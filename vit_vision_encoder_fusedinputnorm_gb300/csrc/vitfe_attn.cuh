@@ -18,6 +18,7 @@ constexpr int kAttnRows = 128;      // rows of one score tile: tokens x the quer
 constexpr int kAttnKeys = 128;      // keys of one block
 constexpr int kAttnSMs = 152;       // GB300; the plan's balance and the capacities derived from it
 constexpr int kAttnMinBlocks = 4;   // key blocks below which a range is not cut
+constexpr int kAttnFewRows = 32;    // score rows up to which pieces are cheap to join
 
 // A query item: up to 2 * tokens-per-tile tokens of one sequence over the key blocks
 // [kb, ke) of it, for one key head at a time.  Rows are token-major: row = token * group + head.
