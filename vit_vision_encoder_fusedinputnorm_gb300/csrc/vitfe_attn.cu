@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   __shared__ int bins[kBins];
   __shared__ unsigned bad;
   __shared__ unsigned long long blocks_total;
-  __shared__ int slots, joins;
+  __shared__ int slots[2], joins;            // of items of many and of few rows
   const int tid = threadIdx.x;
   AttnPlanHdr* hdr = reinterpret_cast<AttnPlanHdr*>(a.plan);
   AttnItem* items = reinterpret_cast<AttnItem*>(a.plan + a.l.at_items);
@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   if (tid == 0) {
     bad = 0xffffffffu;
     blocks_total = 0;
-    slots = joins = 0;
+    slots[0] = joins = 0;
+    slots[1] = (int)a.l.cap_many;
   }
   __syncthreads();
   int n = a.max_seqs;
@@ -163,12 +164,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
   __syncthreads();
   // Items longer than an SM's even share of all blocks are cut: they would be the last to end.  Few rows
-  // (single tokens) are cut at half of it: joining their pieces costs next to nothing, where for whole
-  // tiles it took as long as it saved (71 us beside 107 us, packed prompts up to 4100 rows).
-  const unsigned long long half_share = (blocks_total * (unsigned)a.heads_kv + 2 * kAttnSMs - 1) / (2 * kAttnSMs);
+  // (single tokens) are cut to a sixth of it, for the evenness: joining their pieces costs next to
+  // nothing, where for whole tiles it took as long as it saved (71 us beside 107 us, packed prompts up
+  // to 4100 rows).
+  const unsigned long long all_blocks = blocks_total * (unsigned)a.heads_kv;
   auto pieces_of = [&](const AttnItem& it) {
     if (!a.l.may_split) return 1;
-    const unsigned long long fair = it.qn * a.group <= kAttnFewRows ? half_share : 2 * half_share;
+    const unsigned parts = it.qn * a.group <= kAttnFewRows ? kAttnFewCuts * kAttnSMs : kAttnSMs;
+    const unsigned long long fair = (all_blocks + parts - 1) / parts;
     const int most = (int)(fair > kAttnMinBlocks ? fair : kAttnMinBlocks);
     return it.ke > most ? ceil_div(it.ke, most) : 1;
   };
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
     const int each = ceil_div(len, p);
     int slot = -1;
     if (p > 1) {
-      slot = atomicAdd(&slots, p);
+      slot = atomicAdd(&slots[it.qn * a.group <= kAttnFewRows], p);
       join[atomicAdd(&joins, 1)] = AttnJoin{it.q0, it.qn, slot, p};
     }
     for (int i = 0; i < p; ++i) {
@@ -332,9 +335,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t o_col = tmem + lanes + 256u + (uint32_t)t * 128u;
     const int my_tok = t * tok + row / g, head_in = row % g;
     const float scale2 = a.scale * 1.4426950408889634f;      // exponents of 2
-    const int slot_rows = (int)((a.s.rows_q < 2 * tok ? a.s.rows_q : 2 * tok) * g);
+    const AttnSlots slots(a.s, a.l);
     float2* stat = static_cast<float2*>(a.workspace);
-    float* part = reinterpret_cast<float*>(stat + a.l.cap_slots * hk * (int64_t)slot_rows);
+    float* part = reinterpret_cast<float*>(stat + slots.rows(a.l));
     uint32_t ns = 0, no = 0;                                 // phases of s_full, o_full
     bool ok = true;
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int head = kh * g + head_in;
       const int64_t qrow = (int64_t)it.q0 + my_tok;
-      const int64_t at = ((int64_t)max(it.slot, 0) * hk + kh) * slot_rows + my_tok * g + head_in;
+      const int64_t at = slots.at(max(it.slot, 0), kh) + my_tok * g + head_in;
       for (int c = 0; c < d; c += 16) {
         uint32_t o[16];
         if (n > 0) {
@@ -634,26 +637,37 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   const AttnJoin* joins = reinterpret_cast<const AttnJoin*>(a.plan + a.l.at_joins);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim;
-  const int slot_rows = (int)((a.s.rows_q < 2 * a.l.tok ? a.s.rows_q : 2 * a.l.tok) * g);
+  const AttnSlots slots(a.s, a.l);
   const float2* stat = static_cast<const float2*>(a.workspace);
-  const float* part = reinterpret_cast<const float*>(stat + a.l.cap_slots * hk * (int64_t)slot_rows);
+  const float* part = reinterpret_cast<const float*>(stat + slots.rows(a.l));
   for (int w = blockIdx.x; w < hdr->n_joins * hk; w += gridDim.x) {
     const AttnJoin jn = joins[w / hk];
     const int kh = w % hk;
+    const int64_t first = slots.at(jn.slot, kh), step = slots.step(jn.slot);
     for (int r = warp; r < jn.qn * g; r += 8) {
-      const int64_t at = ((int64_t)jn.slot * hk + kh) * slot_rows + r, step = (int64_t)hk * slot_rows;
+      const int64_t at = first + r;
       float top = -INFINITY;
-      for (int p = 0; p < jn.pieces; ++p) top = fmaxf(top, stat[at + p * step].x);
+      for (int p = lane; p < jn.pieces; p += 32) top = fmaxf(top, stat[at + p * step].x);
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
       const float ref = top == -INFINITY ? 0.f : top;
       float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int p = 0; p < jn.pieces; ++p) {
-        const float2 ml = stat[at + p * step];
-        if (ml.y == 0.f) continue;             // no key of this piece weighs anything (NaN goes on)
-        const float wgt = ml.y * exp2_approx(ml.x - ref);
-        sum += wgt;
+      for (int p0 = 0; p0 < jn.pieces; p0 += 32) {
+        float wgt = 0.f;                       // a piece without a key that weighs anything adds nothing
+        if (p0 + lane < jn.pieces) {
+          const float2 ml = stat[at + (p0 + lane) * step];
+          if (ml.y != 0.f) wgt = ml.y * exp2_approx(ml.x - ref);
+        }
+        sum += warp_sum(wgt);
+        const int n = min(32, jn.pieces - p0);
+#pragma unroll 4
+        for (int p = 0; p < n; ++p) {
+          const float f = __shfl_sync(0xffffffffu, wgt, p);
+          const float* src = part + (at + (p0 + p) * step) * d;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (lane + 32 * i < d) o[i] = fmaf(wgt, part[(at + p * step) * d + lane + 32 * i], o[i]);
+          for (int i = 0; i < 4; ++i)
+            if (lane + 32 * i < d) o[i] = fmaf(f, src[lane + 32 * i], o[i]);
+        }
       }
       const int tok = r / g, head = kh * g + r % g;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;

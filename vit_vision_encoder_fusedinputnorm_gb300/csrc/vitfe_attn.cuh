@@ -18,7 +18,8 @@ constexpr int kAttnRows = 128;      // rows of one score tile: tokens x the quer
 constexpr int kAttnKeys = 128;      // keys of one block
 constexpr int kAttnSMs = 152;       // GB300; the plan's balance and the capacities derived from it
 constexpr int kAttnMinBlocks = 4;   // key blocks below which a range is not cut
-constexpr int kAttnFewRows = 32;    // score rows up to which pieces are cheap to join
+constexpr int kAttnFewRows = 32;    // score rows up to which pieces are cheap to join,
+constexpr int kAttnFewCuts = 6;     // and then made a sixth of an SM's even share
 
 // A query item: up to 2 * tokens-per-tile tokens of one sequence over the key blocks
 // [kb, ke) of it, for one key head at a time.  Rows are token-major: row = token * group + head.
@@ -60,7 +61,8 @@ struct alignas(16) AttnPlanHdr {
 struct AttnLayout {
   int group;              // query heads to a key head
   int tok;                // tokens of one score tile: 128 / group
-  int64_t cap_items, cap_keys, cap_joins, cap_slots;
+  int64_t cap_items, cap_keys, cap_joins;
+  int64_t cap_many, cap_few;   // slots of partial results of items of many and of few rows
   int64_t at_items, at_keys, at_joins, at_scan_q, at_scan_k, bytes;
   bool may_split;         // some sequence may hold more than kAttnMinBlocks key blocks
 };
@@ -71,13 +73,17 @@ inline AttnLayout attn_layout(const vitfe_attention_shape& s) {
   l.tok = kAttnRows / l.group;
   l.may_split = (s.rows_k + kAttnKeys - 1) / kAttnKeys > kAttnMinBlocks;
   const int64_t seqs = (int64_t)s.max_seqs + 1;
-  // pieces beyond one per item: a piece has at least W / (2 SMs) blocks (attn_plan_kernel)
-  const int64_t extra = l.may_split ? 2 * kAttnSMs / s.heads_kv + 1 : 0;
+  // Pieces of items of many rows are as long as an SM's even share of the W blocks of all items and key
+  // heads, of few rows a sixth of it (attn_plan_kernel): at most `n` SM shares make n x SMs / heads
+  // pieces beyond the first of each item, and twice that number of pieces in all.
+  const int64_t many = l.may_split ? kAttnSMs / s.heads_kv + 1 : 0;
+  const int64_t few = l.may_split ? kAttnFewCuts * kAttnSMs / s.heads_kv + 1 : 0;
+  l.cap_many = 2 * many;
+  l.cap_few = 2 * few;
   auto lesser = [](int64_t a, int64_t b) { return a < b ? a : b; };
-  l.cap_items = s.rows_q / (2 * l.tok) + lesser(seqs, s.rows_q) + extra;
+  l.cap_items = s.rows_q / (2 * l.tok) + lesser(seqs, s.rows_q) + many + few;
   l.cap_keys = s.rows_k / kAttnKeys + lesser(seqs, s.rows_k);
-  l.cap_joins = extra;
-  l.cap_slots = 2 * extra;
+  l.cap_joins = many + few;
   int64_t at = sizeof(AttnPlanHdr);
   auto take = [&](int64_t n) {
     const int64_t r = at;
@@ -93,15 +99,29 @@ inline AttnLayout attn_layout(const vitfe_attention_shape& s) {
   return l;
 }
 
-// Rows of one slot of partial results, and the workspace of the forward pass.
-inline int64_t attn_slot_rows(const vitfe_attention_shape& s) {
-  const int64_t g = s.heads_q / s.heads_kv, t = kAttnRows / g;
-  const int64_t rows = (s.rows_q < 2 * t ? s.rows_q : 2 * t) * g;
-  return rows;
+// Rows of a slot of an item of many rows.
+__host__ __device__ inline int64_t attn_slot_rows(const vitfe_attention_shape& s, int tok, int group) {
+  return (s.rows_q < 2 * tok ? s.rows_q : 2 * tok) * group;
 }
+// First row of a slot of one key head, in the workspace's [rows] of (maximum, sum) and of outputs; the
+// slots of an item's pieces follow each other heads_kv slots on.
+struct AttnSlots {
+  int64_t rows_many, base_few;
+  int cap_many, hk;
+  __host__ __device__ AttnSlots(const vitfe_attention_shape& s, const AttnLayout& l)
+      : rows_many(attn_slot_rows(s, l.tok, l.group)), cap_many((int)l.cap_many), hk(s.heads_kv) {
+    base_few = l.cap_many * hk * rows_many;
+  }
+  __host__ __device__ int64_t rows(const AttnLayout& l) const { return base_few + l.cap_few * hk * kAttnFewRows; }
+  __host__ __device__ int64_t step(int slot) const { return slot < cap_many ? hk * rows_many : (int64_t)hk * kAttnFewRows; }
+  __host__ __device__ int64_t at(int slot, int kh) const {
+    return slot < cap_many ? ((int64_t)slot * hk + kh) * rows_many
+                           : base_few + ((int64_t)(slot - cap_many) * hk + kh) * kAttnFewRows;
+  }
+};
 inline int64_t attn_workspace(const vitfe_attention_shape& s) {
   const AttnLayout l = attn_layout(s);
-  return (l.cap_slots * s.heads_kv * attn_slot_rows(s) * (s.head_dim + 2) * 4 + 15) / 16 * 16;
+  return l.may_split ? (AttnSlots(s, l).rows(l) * (s.head_dim + 2) * 4 + 15) / 16 * 16 : 0;
 }
 inline int64_t attn_backward_workspace(const vitfe_attention_shape& s) {
   return (s.rows_q * s.heads_q * 8 + 15) / 16 * 16;   // two floats a row and head

@@ -156,11 +156,51 @@ struct MropeKernelArgs {
 // angle does, exactly, so no position loses accuracy: the phase's top 32 bits are the angle
 // to 2^-32 turns.
 template <typename X, int V>
-__global__ void __launch_bounds__(kThreads) mrope_kernel(const MropeKernelArgs a, const __grid_constant__ MropeTable tab) {
-  extern __shared__ float cs[];                  // [rows_per_block][2][half]
+__global__ void __launch_bounds__(kThreads, 4) mrope_kernel(const __grid_constant__ MropeKernelArgs a, const __grid_constant__ MropeTable tab) {
+  extern __shared__ __align__(16) float cs[];    // [rows_per_block][2][half]; half is a multiple of 4
   const int r0 = blockIdx.x * a.rows_per_block;
   const int nr = min(a.rows_per_block, a.rows - r0);
-  for (int i = threadIdx.x; i < nr * a.half; i += kThreads) {
+  using XV = Vec<X, V>;
+  constexpr int kRows = V == 8 ? 2 : 4;          // rows of a thread in flight
+  // unit: (head, group of V pairs), then the copied tail of each head.  A thread keeps its unit over
+  // the block's rows; with fewer units than threads, the threads share out the rows as well.
+  const int threads = (int)blockDim.x, rot = a.half / V;
+  const int lanes = a.units < threads ? a.units : threads, side = threads / lanes;
+  const int r_first = threadIdx.x / lanes;
+  int u = blockIdx.y * threads + threadIdx.x % lanes;
+  if (r_first >= side) u = a.units;
+  const X* x = nullptr;
+  X* y = nullptr;
+  long long xs = 0, ys = 0;
+  int g = 0;
+  bool turn = false;
+  XV va[kRows], vb[kRows];
+  auto place = [&]() {
+    const int which = u >= a.units_q;
+    const int v = u - (which ? a.units_q : 0), head = v / a.groups;
+    g = v - head * a.groups;
+    turn = g < rot;
+    xs = a.x_stride[which];
+    ys = a.y_stride[which];
+    const int at = head * a.head_dim + (turn ? g * V : 2 * a.half + (g - rot) * V);
+    x = static_cast<const X*>(a.x[which]) + r0 * xs + at;
+    y = static_cast<X*>(a.y[which]) + r0 * ys + at;
+  };
+  auto fetch = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int rr = r + i * side;
+      if (rr < nr) {
+        va[i] = *reinterpret_cast<const XV*>(x + rr * xs);
+        if (turn) vb[i] = *reinterpret_cast<const XV*>(x + rr * xs + a.half);
+      }
+    }
+  };
+  if (u < a.units) {                             // the first rows are on their way while the table is made
+    place();
+    fetch(r_first);
+  }
+  for (int i = threadIdx.x; i < nr * a.half; i += threads) {
     const int r = i / a.half, p = i - r * a.half;
     const int64_t at = a.pos[(size_t)tab.axis[p] * a.rows + r0 + r];
     const uint64_t phase = (uint64_t)at * tab.turn[p];
@@ -171,34 +211,36 @@ __global__ void __launch_bounds__(kThreads) mrope_kernel(const MropeKernelArgs a
     cs[(2 * r + 1) * a.half + p] = sn * a.sign;
   }
   __syncthreads();
-  using XV = Vec<X, V>;
-  // unit: (row, head, group of V pairs), then the copied tail of each head
-  const int per_row = a.units;
-  for (int u = blockIdx.y * kThreads + threadIdx.x; u < nr * per_row; u += gridDim.y * kThreads) {
-    const int r = u / per_row;
-    int v = u - r * per_row;
-    const int which = v >= a.units_q;
-    v -= which ? a.units_q : 0;
-    const int head = v / a.groups, g = v - head * a.groups;
-    const X* x = static_cast<const X*>(a.x[which]) + (long long)(r0 + r) * a.x_stride[which] + (long long)head * a.head_dim;
-    X* y = static_cast<X*>(a.y[which]) + (long long)(r0 + r) * a.y_stride[which] + (long long)head * a.head_dim;
-    const int rot = a.half / V;
-    if (g < rot) {
-      const float* c = cs + (size_t)(2 * r) * a.half + g * V;
-      const XV va = *reinterpret_cast<const XV*>(x + g * V);
-      const XV vb = *reinterpret_cast<const XV*>(x + a.half + g * V);
-      XV ya, yb;
+  for (bool first = true; u < a.units; u += gridDim.y * threads) {
+    if (!first) place();
+    for (int r = r_first; r < nr; r += kRows * side) {
+      if (!first) fetch(r);
+      first = false;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float fa = to_f32(va.v[e]), fb = to_f32(vb.v[e]);
-        ya.v[e] = from_f32<X>(fmaf(fa, c[e], -(fb * c[a.half + e])));
-        yb.v[e] = from_f32<X>(fmaf(fb, c[e], fa * c[a.half + e]));
+      for (int i = 0; i < kRows; ++i) {
+        const int rr = r + i * side;
+        if (rr >= nr) break;
+        if (turn) {
+          const float4* c = reinterpret_cast<const float4*>(cs + 2 * rr * a.half + g * V);
+          const float4* s = reinterpret_cast<const float4*>(cs + (2 * rr + 1) * a.half + g * V);
+          XV ya, yb;
+#pragma unroll
+          for (int q = 0; q < V; q += 4) {
+            const float4 c4 = c[q / 4], s4 = s[q / 4];
+            const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float fa = to_f32(va[i].v[q + e]), fb = to_f32(vb[i].v[q + e]);
+              ya.v[q + e] = from_f32<X>(fmaf(fa, cc[e], -(fb * ss[e])));
+              yb.v[q + e] = from_f32<X>(fmaf(fb, cc[e], fa * ss[e]));
+            }
+          }
+          *reinterpret_cast<XV*>(y + rr * ys) = ya;
+          *reinterpret_cast<XV*>(y + rr * ys + a.half) = yb;
+        } else {
+          *reinterpret_cast<XV*>(y + rr * ys) = va[i];
+        }
       }
-      *reinterpret_cast<XV*>(y + g * V) = ya;
-      *reinterpret_cast<XV*>(y + a.half + g * V) = yb;
-    } else {
-      const int c = 2 * a.half + (g - rot) * V;
-      *reinterpret_cast<XV*>(y + c) = *reinterpret_cast<const XV*>(x + c);
     }
   }
 }
@@ -224,19 +266,21 @@ cudaError_t launch_typed(const MropeArgs& a, const MropeTable& tab, cudaStream_t
   k.units = (a.heads[0] + a.heads[1]) * k.groups;
   k.sign = a.inverse ? -1.f : 1.f;
   if (k.units == 0) return cudaSuccess;
-  int per = (4 * kThreads + k.units - 1) / k.units;
+  // as many threads as share the units (or the rows, where there are few units) out evenly; four rows
+  // to a thread, as far as the block's table of sines (32 KB) reaches; few rows: one to a block and
+  // its heads over grid.y, so that more SMs take part
+  const int passes = (k.units + kThreads - 1) / kThreads, side = passes > 1 ? 1 : kThreads / k.units;
+  const int threads = ((k.units * side + passes - 1) / passes + 31) / 32 * 32;
   const int room = 8192 / (2 * k.half);
-  per = per < 1 ? 1 : per > room ? room : per;
-  // few rows: one row per block and its heads over grid.y, so that more SMs take part
-  int ysplit = 1;
-  if (a.rows < 152 * 2) {
+  int per = 4 * side < room ? 4 * side : room, ysplit = 1;
+  if (a.rows < 2 * 152) {
     per = 1;
-    ysplit = (k.units + kThreads - 1) / kThreads;
+    ysplit = (k.units + threads - 1) / threads;
     ysplit = ysplit > 16 ? 16 : ysplit;
   }
   k.rows_per_block = per;
   const dim3 grid((unsigned)((a.rows + per - 1) / per), (unsigned)ysplit);
-  mrope_kernel<X, V><<<grid, kThreads, (size_t)per * 2 * k.half * sizeof(float), s>>>(k, tab);
+  mrope_kernel<X, V><<<grid, threads, (size_t)per * 2 * k.half * sizeof(float), s>>>(k, tab);
   return cudaGetLastError();
 }
 

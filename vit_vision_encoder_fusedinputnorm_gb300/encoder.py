@@ -15,7 +15,6 @@ any other call.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional, Sequence
 
 import torch
@@ -23,13 +22,19 @@ import torch
 from . import binding as B
 
 _DTYPES = {torch.bfloat16: B.VITFE_BF16, torch.float16: B.VITFE_F16, torch.float32: B.VITFE_F32}
+_float32 = torch.float32
+_empty, _empty_like = torch.empty, torch.empty_like
+_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
+
+# A call of these costs a few microseconds beside kernels that may take as few, so the helpers below
+# are kept short, and the wrappers call the library's entry points themselves.
 
 def _dtype(t: torch.Tensor) -> int:
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"bfloat16, float16 or float32 tensors are supported, not {t.dtype}") from None
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"bfloat16, float16 or float32 tensors are supported, not {t.dtype}")
+    return code
 
 
 def _current(stream):
@@ -39,9 +44,12 @@ def _current(stream):
 
 def _launch(name: str, device: int, *args) -> None:
     """Call an entry point on the current stream of ``device``."""
-    guard = contextlib.nullcontext() if device == torch.cuda.current_device() else torch.cuda.device(device)
-    with guard:
-        code = getattr(B.load(), name)(*args, torch._C._cuda_getCurrentRawStream(device))
+    entry = getattr(B.load(), name)
+    if device == _get_device():
+        code = entry(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            code = entry(*args, _raw_stream(device))
     if code:
         raise B.VitfeError(name, code)
 
@@ -65,8 +73,10 @@ def _rows(x: torch.Tensor, name: str) -> int:
     """Row stride of a [rows][width] tensor whose rows are contiguous."""
     if x.dim() != 2:
         raise ValueError(f"{name}: a [rows][width] tensor is needed, not {tuple(x.shape)}")
-    rows, width = x.shape
     row, col = x.stride()
+    if col == 1 and row >= x.shape[1]:
+        return row
+    rows, width = x.shape
     if col != 1 and rows and width > 1:
         raise ValueError(f"{name}: its rows have to be contiguous")
     return row if rows > 1 else width
@@ -84,7 +94,7 @@ def _heads(x: torch.Tensor, name: str) -> int:
 
 
 def _like(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return _empty_like(x) if x.is_contiguous() else _empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _target(x: torch.Tensor, out: Optional[torch.Tensor], name: str) -> torch.Tensor:
@@ -95,10 +105,11 @@ def _target(x: torch.Tensor, out: Optional[torch.Tensor], name: str) -> torch.Te
     return out
 
 
-def _vector(v: Optional[torch.Tensor], width: int, name: str, dtype: Optional[torch.dtype] = None) -> None:
-    if v is not None and (v.dim() != 1 or v.shape[0] != width or not v.is_contiguous()
-                          or (dtype is not None and v.dtype != dtype)):
+def _vector(v: torch.Tensor, width: int, name: str, dtype: Optional[torch.dtype] = None) -> int:
+    """Address of a contiguous [width] tensor."""
+    if v.dim() != 1 or v.shape[0] != width or not v.is_contiguous() or (dtype is not None and v.dtype != dtype):
         raise ValueError(f"{name}: a contiguous [{width}] tensor{f' of {dtype}' if dtype else ''} is needed")
+    return v.data_ptr()
 
 
 # ------------------------------------------------------------------ layer norm
@@ -111,18 +122,27 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stats: bo
     stride = _rows(x, "x")
     rows, width = x.shape
     device = _device(x, weight, bias, out)
-    _vector(weight, width, "weight")
-    _vector(bias, width, "bias", None if weight is None else weight.dtype)
-    out = _target(x, out, "out")
-    mean = rstd = None
-    if stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-    params = weight if weight is not None else bias
-    _launch("vitfe_layer_norm", device, x.data_ptr(), stride, _dtype(x), rows, width, _ptr(weight), _ptr(bias),
-            B.VITFE_F32 if params is None else _dtype(params), eps, out.data_ptr(), _rows(out, "out"), _ptr(mean),
-            _ptr(rstd))
-    return (out, mean, rstd) if stats else out
+    w = b = None
+    kind = B.VITFE_F32
+    if weight is not None:
+        w, kind = _vector(weight, width, "weight"), _dtype(weight)
+    if bias is not None:
+        b = _vector(bias, width, "bias", None if weight is None else weight.dtype)
+        kind = _dtype(bias)
+    if out is None:
+        out = _like(x)
+        out_stride = width
+    else:
+        out_stride = _rows(_target(x, out, "out"), "out")
+    if not stats:
+        _launch("vitfe_layer_norm", device, x.data_ptr(), stride, _dtype(x), rows, width, w, b, kind, eps,
+                out.data_ptr(), out_stride, None, None)
+        return out
+    mean = _empty(rows, dtype=_float32, device=x.device)
+    rstd = _empty_like(mean)
+    _launch("vitfe_layer_norm", device, x.data_ptr(), stride, _dtype(x), rows, width, w, b, kind, eps, out.data_ptr(),
+            out_stride, mean.data_ptr(), rstd.data_ptr())
+    return out, mean, rstd
 
 
 def layer_norm_backward(dout, x, mean, rstd, weight=None, params: bool = True, stream=None):
@@ -135,20 +155,20 @@ def layer_norm_backward(dout, x, mean, rstd, weight=None, params: bool = True, s
     device = _device(x, dout, mean, rstd, weight)
     if dout.shape != x.shape or dout.dtype != x.dtype:
         raise ValueError("dout: x's shape and type are needed")
-    _vector(weight, width, "weight")
-    _vector(mean, rows, "mean", torch.float32)
-    _vector(rstd, rows, "rstd", torch.float32)
+    w, kind = (None, B.VITFE_F32) if weight is None else (_vector(weight, width, "weight"), _dtype(weight))
+    m, r = _vector(mean, rows, "mean", _float32), _vector(rstd, rows, "rstd", _float32)
     dx = _like(x)
-    dweight = dbias = work = None
-    size = 0
-    if params:
-        dweight = torch.empty(width, dtype=torch.float32, device=x.device)
-        dbias = torch.empty_like(dweight)
-        size = B.vitfe_layer_norm_workspace(rows, width)
-        work = torch.empty(size, dtype=torch.uint8, device=x.device)
+    if not params:
+        _launch("vitfe_layer_norm_backward", device, dout.data_ptr(), _rows(dout, "dout"), x.data_ptr(), stride,
+                _dtype(x), rows, width, w, kind, m, r, dx.data_ptr(), width, None, None, None, 0)
+        return dx, None, None
+    dweight = _empty(width, dtype=_float32, device=x.device)
+    dbias = _empty_like(dweight)
+    size = B.vitfe_layer_norm_workspace(rows, width)
+    work = _empty(size, dtype=torch.uint8, device=x.device)
     _launch("vitfe_layer_norm_backward", device, dout.data_ptr(), _rows(dout, "dout"), x.data_ptr(), stride, _dtype(x),
-            rows, width, _ptr(weight), B.VITFE_F32 if weight is None else _dtype(weight), mean.data_ptr(),
-            rstd.data_ptr(), dx.data_ptr(), width, _ptr(dweight), _ptr(dbias), _ptr(work), size)
+            rows, width, w, kind, m, r, dx.data_ptr(), width, dweight.data_ptr(), dbias.data_ptr(), work.data_ptr(),
+            size)
     return dx, dweight, dbias
 
 
@@ -249,7 +269,7 @@ class AttentionPlan:
         self._q, self._k = (rows_q, heads_q, head_dim), (rows_k, heads_kv, head_dim)
         self._work = B.vitfe_attention_workspace(self.shape)
         self._work_backward = B.vitfe_attention_backward_workspace(self.shape)
-        with contextlib.nullcontext() if stream is None else _current(stream):
+        with _current(stream if stream is not None else torch.cuda.current_stream(cu_q.device)):
             size = B.vitfe_attention_plan_bytes(self.shape)
             self.buffer = torch.empty(max(size, 16), dtype=torch.uint8, device=cu_q.device)
             self.update(cu_q, cu_k, status)
@@ -287,8 +307,8 @@ def attention(q, k, v, plan: AttentionPlan, scale: Optional[float] = None, lse: 
     shape = plan.of(q, k, v)
     device = _device(plan.buffer, q, k, v, out, status)
     out = _target(q, out, "out")
-    sums = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse else None
-    work = torch.empty(plan._work, dtype=torch.uint8, device=q.device) if plan._work else None
+    sums = _empty(plan._q[:2], dtype=_float32, device=q.device) if lse else None
+    work = _empty(plan._work, dtype=torch.uint8, device=q.device) if plan._work else None
     _launch("vitfe_attention", device, shape, plan.buffer.data_ptr(), q.data_ptr(), _heads(q, "q"), k.data_ptr(),
             _heads(k, "k"), v.data_ptr(), _heads(v, "v"), q.shape[2] ** -0.5 if scale is None else scale,
             out.data_ptr(), _heads(out, "out"), _ptr(sums), _ptr(work), _ptr(status))
@@ -309,7 +329,7 @@ def attention_backward(dout, q, k, v, out, lse, plan: AttentionPlan, scale: Opti
     if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse: the forward pass's float32 [rows][heads] is needed")
     dq, dk, dv = _like(q), _like(k), _like(v)
-    work = torch.empty(plan._work_backward, dtype=torch.uint8, device=q.device) if plan._work_backward else None
+    work = _empty(plan._work_backward, dtype=torch.uint8, device=q.device) if plan._work_backward else None
     _launch("vitfe_attention_backward", device, shape, plan.buffer.data_ptr(), dout.data_ptr(), _heads(dout, "dout"),
             q.data_ptr(), _heads(q, "q"), k.data_ptr(), _heads(k, "k"), v.data_ptr(), _heads(v, "v"), out.data_ptr(),
             _heads(out, "out"), lse.data_ptr(), q.shape[2] ** -0.5 if scale is None else scale, dq.data_ptr(),
