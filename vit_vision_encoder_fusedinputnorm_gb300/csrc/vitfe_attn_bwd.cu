@@ -28,6 +28,7 @@ struct alignas(8) RowValue {
 
 template <typename T>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnArgs a) {
+  grid_dep_trigger();
   if (a.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {   // a wait that runs out overrides it later
     a.status[0] = kOk;
     a.status[1] = -1;
@@ -209,6 +210,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // ring rows that no load writes (a group that does not divide 128)
   if (tok * g < kAttnRows && warp < (int)(ring.a + ring.b)) zero_tile_rows(ring_a + (uint32_t)warp * tile_bytes, nb, tok * g);
   __syncthreads();
+  // The row values are there; and with them the next kernel of this call may start, on the SMs that this
+  // one leaves.
+  grid_dep_wait();
+  grid_dep_trigger();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t st_col = tmem, dpt_col = tmem + 128u, dv_col = tmem + 256u, dk_col = tmem + 384u;
@@ -706,6 +711,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&sh.a_full[sa]));
     }
   }
+  // It may have started beside the kernel before it (which had seen the row values), but ends after it, so
+  // that what follows on the stream finds both done.
+  grid_dep_wait();
   bwd_end(sh, tmem, a.status);
 }
 
@@ -739,15 +747,30 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
     md = mk = mv = mq;
   }
   const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   if (s.rows_k > 0) {
     e = allow_smem(reinterpret_cast<const void*>(attn_keys_kernel<T>), kSmemMax - 3072, allowed_keys);
     if (e != cudaSuccess) return e;
-    attn_keys_kernel<T><<<(unsigned)(wk < sms ? wk : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, ring);
+    cfg.gridDim = dim3((unsigned)(wk < sms ? wk : sms));
+    e = cudaLaunchKernelEx(&cfg, attn_keys_kernel<T>, a, mq, md, mk, mv, ring);
+    if (e != cudaSuccess) return e;
+  } else {
+    cfg.numAttrs = 0;      // right behind the row values: it waits for them in full
   }
   if (s.rows_q > 0) {
     e = allow_smem(reinterpret_cast<const void*>(attn_queries_kernel<T>), kSmemMax - 3072, allowed_queries);
     if (e != cudaSuccess) return e;
-    attn_queries_kernel<T><<<(unsigned)(wq < sms ? wq : sms), kBwdThreads, smem, st>>>(a, mq, md, mk, mv, ring);
+    cfg.gridDim = dim3((unsigned)(wq < sms ? wq : sms));
+    e = cudaLaunchKernelEx(&cfg, attn_queries_kernel<T>, a, mq, md, mk, mv, ring);
+    if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
