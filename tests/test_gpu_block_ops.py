@@ -279,6 +279,8 @@ ATTN_CASES = [  # lens_q, lens_k (None: the same), q heads, k heads, head_dim, c
     ([64] * 40, None, 1, 1, 40, False, 0),
     ([1100], None, 1, 1, 88, True, 0),
     ([], [], 2, 2, 64, False, 17),                           # nothing but padding
+    ([1] * 30 + [300, 0, 140], [700] * 20 + [90] * 10 + [300, 5, 1000], 4, 2, 128, True, 3),  # short and long ones
+    ([70, 1, 200, 0] * 12, None, 2, 2, 80, False, 5),
 ]
 
 

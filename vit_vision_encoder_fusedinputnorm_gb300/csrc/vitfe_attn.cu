@@ -10,7 +10,7 @@ constexpr int kBins = 1024;
 struct PlanArgs {
   const int32_t* cu_q;
   const int32_t* cu_k;
-  int rows_q, rows_k, max_seqs, heads_kv, group, tok2, causal;
+  int rows_q, rows_k, max_seqs, heads_kv, group, item_tok, causal;
   AttnLayout l;
   char* plan;
   int32_t* status;
@@ -55,9 +55,9 @@ __device__ AttnItem query_item(const PlanArgs& a, const int* scan, int n, int t)
   const int s = find_item(scan, n + 1, t);
   const int2 q = seq_rows(a.cu_q, n, s, a.rows_q);
   AttnItem it;
-  const int first = (t - scan[s]) * a.tok2;
+  const int first = (t - scan[s]) * a.item_tok;
   it.q0 = q.x + first;
-  it.qn = min(a.tok2, q.y - it.q0);
+  it.qn = min(a.item_tok, q.y - it.q0);
   it.k0 = 0;
   it.kn = 0;
   if (s < n) {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
     int cq = 0, ck = 0;
     if (s <= n) {
       const int2 q = seq_rows(a.cu_q, n, s, a.rows_q), k = seq_rows(a.cu_k, n, s, a.rows_k);
-      cq = ceil_div(q.y - q.x, a.tok2);
+      cq = ceil_div(q.y - q.x, a.item_tok);
       ck = ceil_div(k.y - k.x, kAttnKeys);
     }
     int total;
@@ -164,9 +164,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
   __syncthreads();
   // Items longer than an SM's even share of all blocks are cut: they would be the last to end.  Few rows
-  // (single tokens) are cut to a sixth of it, for the evenness: joining their pieces costs next to
-  // nothing, where for whole tiles it took as long as it saved (71 us beside 107 us, packed prompts up
-  // to 4100 rows).
+  // (single tokens) are cut to a fourth of it, which is half of what each of an SM's two tiles gets, for
+  // the evenness (64 tokens over 1..32,768 keys, 8 over 8,192: a half 163/77 us, a third 156/63, a fourth
+  // 159/60, a sixth 164/68, a twelfth 183/77).  Joining their pieces costs next to nothing, where for
+  // whole tiles it took as long as it saved (71 us beside 107 us, packed prompts up to 4100 rows).
   const unsigned long long all_blocks = blocks_total * (unsigned)a.heads_kv;
   auto pieces_of = [&](const AttnItem& it) {
     if (!a.l.may_split) return 1;
@@ -272,13 +273,33 @@ __device__ __forceinline__ int tile_blocks(const AttnItem& it, int t, int tok, b
   return max(0, min(it.ke, ceil_div(last, kAttnKeys)) - it.kb);
 }
 
-// The w-th of this CTA's works: the list is sorted longest first and dealt back and forth, so
-// that the SMs' sums come out even.
-__device__ __forceinline__ int deal(int round) {
-  return round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+// The w-th work of worker `id` of n: the list is sorted longest first and dealt back and forth, so that
+// the workers' sums come out even.
+__device__ __forceinline__ int deal(int round, int id, int n) { return round * n + ((round & 1) ? n - 1 - id : id); }
+
+// The blocks of a worker's works, one after the other (works without any are passed over).
+struct WorkStream {
+  AttnItem it;
+  int kh, n, j, round;
+  bool live;
+};
+__device__ __forceinline__ void next_work(WorkStream& s, const AttnItem* items, int works, int hk, int id, int workers,
+                                          int tok, bool causal) {
+  s.live = false;
+  s.j = 0;
+  for (;;) {
+    const int w = deal(++s.round, id, workers);
+    if (w >= works) return;
+    s.it = items[w / hk];
+    s.kh = w % hk;
+    s.n = tile_blocks(s.it, 0, tok, causal);
+    if (s.n > 0) break;
+  }
+  s.live = true;
 }
 
-template <typename T>
+// kSingle: items of one tile, and each of the two tiles works through items of its own.
+template <typename T, bool kSingle>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, int stages) {
@@ -323,7 +344,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const uint32_t tmem = sh.tmem;
   const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
   const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
-  const int works = hdr->n_items * hk;
+  const int works = hdr->n_items * hk, workers = (kSingle ? 2 : 1) * (int)gridDim.x;
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax and output
@@ -333,18 +354,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)t * 128u;
     const uint32_t o_col = tmem + lanes + 256u + (uint32_t)t * 128u;
-    const int my_tok = t * tok + row / g, head_in = row % g;
+    const int tile = kSingle ? 0 : t, id = kSingle ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;
+    const int my_tok = tile * tok + row / g, head_in = row % g;
     const float scale2 = a.scale * 1.4426950408889634f;      // exponents of 2
     const AttnSlots slots(a.s, a.l);
     float2* stat = static_cast<float2*>(a.workspace);
     float* part = reinterpret_cast<float*>(stat + slots.rows(a.l));
     uint32_t ns = 0, no = 0;                                 // phases of s_full, o_full
     bool ok = true;
-    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+    for (int r = 0, w = deal(0, id, workers); ok && w < works; w = deal(++r, id, workers)) {
       const AttnItem it = items[w / hk];
       const int kh = w % hk;
-      if (it.qn <= t * tok) continue;
-      const int n = tile_blocks(it, t, tok, causal);
+      if (it.qn <= tile * tok) continue;
+      const int n = tile_blocks(it, tile, tok, causal);
       const bool live = row < tok * g && my_tok < it.qn;
       int lim = causal ? min(it.kn, it.off + my_tok + 1) : it.kn;   // keys that the row sees
       if (!live) lim = 0;
@@ -484,11 +506,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         mbar_arrive_expect_tx(bar, q_bytes);
         for (int b = 0; b < nb; ++b)
           tma_load_3d(tiles + (uint32_t)t * tile_bytes + (uint32_t)b * kColBlockBytes, &map_q, bar, b * kColBlock,
-                      kh * g, it.q0 + t * tok);
+                      kh * g, it.q0 + (kSingle ? 0 : t * tok));
         ++nq[t];
         return true;
       };
-      for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+      if constexpr (kSingle) {
+        WorkStream s[2];
+        auto begin = [&](int t) {      // the next work's Q and first K
+          next_work(s[t], items, works, hk, 2 * (int)blockIdx.x + t, workers, tok, causal);
+          if (s[t].live) ok = load_q(s[t].it, s[t].kh, t) && load(&map_k, s[t].kh, s[t].it.k0 + s[t].it.kb * kAttnKeys);
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          s[t].round = -1;
+          if (ok) begin(t);
+        }
+        while (ok && (s[0].live || s[1].live)) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || !s[t].live) continue;
+            const int key = s[t].it.k0 + (s[t].it.kb + s[t].j) * kAttnKeys;
+            ok = load(&map_v, s[t].kh, key);
+            if (!ok) continue;
+            if (++s[t].j < s[t].n) ok = load(&map_k, s[t].kh, key + kAttnKeys);
+            else begin(t);
+          }
+        }
+      }
+      for (int r = 0, w = deal(0, blockIdx.x, workers); !kSingle && ok && w < works; w = deal(++r, blockIdx.x, workers)) {
         const AttnItem it = items[w / hk];
         const int kh = w % hk;
         const int n0 = tile_blocks(it, 0, tok, causal), n1 = tile_blocks(it, 1, tok, causal);
@@ -549,7 +594,52 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       __syncwarp();
     };
-    for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
+    if constexpr (kSingle) {
+      // tiles in the order that the loads come in: K0 of each, then V(j) and the next K of each in turn
+      WorkStream s[2];
+      RingPos pos;
+      auto begin = [&](int t) {
+        next_work(s[t], items, works, hk, 2 * (int)blockIdx.x + t, workers, tok, causal);
+        s[t].n = uniform(s[t].n);
+        s[t].live = uniform(s[t].live) != 0;
+        if (s[t].live) {
+          wait(&sh.q_full[t], nq[t]++ & 1u);
+          tc_fence_after();
+        }
+      };
+      auto next_scores = [&](int t) {
+        if (!ok || !s[t].live) return;
+        const RingPos k = pos;
+        pos = pos.next(nst);
+        if (wait(&sh.kv_full[k.i], k.parity))
+          scores(t, k.i, s[t].j + 1 == s[t].n ? &sh.q_empty[t] : nullptr, &sh.kv_empty[k.i]);
+      };
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        s[t].round = -1;
+        begin(t);
+        next_scores(t);
+      }
+      while (ok && (s[0].live || s[1].live)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || !s[t].live) continue;
+          const RingPos v = pos;
+          pos = pos.next(nst);
+          if (!wait(&sh.kv_full[v.i], v.parity)) continue;
+          const int have = uniform(s[t].it.kn - (s[t].it.kb + s[t].j) * kAttnKeys);      // as below
+          if (have < kAttnKeys) zero_tile_rows(ring + v.i * tile_bytes, nb, have);
+          if (!wait(&sh.p_full[t], np[t]++ & 1u)) continue;
+          tc_fence_after();
+          const bool last = s[t].j + 1 == s[t].n;
+          output(t, v.i, s[t].j == 0, last ? &sh.o_full[t] : nullptr, &sh.kv_empty[v.i]);
+          if (last) begin(t);
+          else ++s[t].j;
+          next_scores(t);
+        }
+      }
+    }
+    for (int r = 0, w = deal(0, blockIdx.x, workers); !kSingle && ok && w < works; w = deal(++r, blockIdx.x, workers)) {
       const AttnItem it = items[w / hk];
       const int n0 = uniform(tile_blocks(it, 0, tok, causal)), n1 = uniform(tile_blocks(it, 1, tok, causal));
       const int n = max(n0, n1), keys = uniform(it.kn - it.kb * kAttnKeys);
@@ -681,7 +771,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   }
 }
 
-template <typename T>
+template <typename T, bool kSingle>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   const vitfe_attention_shape& s = a.s;
   CUtensorMap mq, mk, mv;
@@ -701,10 +791,10 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   int sms = 0;
   cudaError_t e = current_sms(&sms);
   if (e == cudaSuccess)
-    e = allow_smem(reinterpret_cast<const void*>(attn_kernel<T>), kSmemMax - (int)sizeof(FwdShared), allowed, kFwdRegs);
+    e = allow_smem(reinterpret_cast<const void*>(attn_kernel<T, kSingle>), kSmemMax - (int)sizeof(FwdShared), allowed, kFwdRegs);
   if (e != cudaSuccess) return e;
-  const int64_t work = a.l.cap_items * s.heads_kv;
-  attn_kernel<T><<<(unsigned)(work < sms ? work : sms), kFwdThreads, smem, st>>>(a, mq, mk, mv, stages);
+  const int64_t work = (a.l.cap_items * s.heads_kv + (kSingle ? 1 : 0)) / (kSingle ? 2 : 1);
+  attn_kernel<T, kSingle><<<(unsigned)(work < sms ? work : sms), kFwdThreads, smem, st>>>(a, mq, mk, mv, stages);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.l.may_split) return e;
   cudaLaunchConfig_t cfg = {};
@@ -732,7 +822,7 @@ cudaError_t launch_attention_plan(const vitfe_attention_shape& s, const int32_t*
   a.max_seqs = s.max_seqs;
   a.heads_kv = s.heads_kv;
   a.group = a.l.group;
-  a.tok2 = 2 * a.l.tok;
+  a.item_tok = a.l.tiles * a.l.tok;
   a.causal = s.causal;
   a.plan = static_cast<char*>(plan);
   a.status = status;
@@ -745,7 +835,9 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
     if (a.status != nullptr) status_ok_kernel<<<1, 1, 0, st>>>(a.status);
     return cudaGetLastError();
   }
-  return a.s.dtype == VITFE_F16 ? launch_typed<__half>(a, st) : launch_typed<__nv_bfloat16>(a, st);
+  if (a.l.tiles == 1)
+    return a.s.dtype == VITFE_F16 ? launch_typed<__half, true>(a, st) : launch_typed<__nv_bfloat16, true>(a, st);
+  return a.s.dtype == VITFE_F16 ? launch_typed<__half, false>(a, st) : launch_typed<__nv_bfloat16, false>(a, st);
 }
 
 }  // namespace vitfe

@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t dp_col = tmem + 256u, dq_col = tmem + 384u;    // S buffers: tmem, tmem + 128
   const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
   const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
-  const int works = hdr->n_items * hk * 2;                      // (item, key head, tile)
+  const int per = a.l.tiles;                                    // score tiles of an item
+  const int works = hdr->n_items * hk * per;                    // (item, key head, tile)
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {             // by a whole warp
     ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
@@ -528,8 +529,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const RowValue* rows = static_cast<const RowValue*>(a.workspace);
     uint32_t i = 0, acc = 0;
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
-      const AttnItem it = items[w / (2 * hk)];
-      const int t = w & 1, kh = (w >> 1) % hk;
+      const AttnItem it = items[w / (per * hk)];
+      const int t = w % per, kh = w / per % hk;
       if (it.kb > 0 || it.qn <= t * tok) continue;
       const int n = key_blocks(it, t, tok, causal);
       const int my_tok = t * tok + row / g, head = kh * g + row % g;
@@ -600,8 +601,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         return true;
       };
       for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
-        const AttnItem it = items[w / (2 * hk)];
-        const int t = w & 1, kh = (w >> 1) % hk;
+        const AttnItem it = items[w / (per * hk)];
+        const int t = w % per, kh = w / per % hk;
         const int nk = key_blocks(it, t, tok, causal);
         if (nk == 0) continue;
         if (!mbar_wait(smem_u32(&sh.kv_empty), (np & 1u) ^ 1u, abort_flag, kAttnWaitNs)) {
@@ -655,8 +656,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       __syncwarp();
     };
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
-      const AttnItem it = items[w / (2 * hk)];
-      const int n = uniform(key_blocks(it, w & 1, tok, causal));
+      const AttnItem it = items[w / (per * hk)];
+      const int n = uniform(key_blocks(it, w % per, tok, causal));
       if (n == 0) continue;
       if (first) {
         if (!wait(&sh.kv_full, np++ & 1u) || !s_of(pa, i) || !wait(&sh.b_full[pb.i], pb.parity)) break;
@@ -698,8 +699,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // 0 * NaN is NaN)
     uint32_t na = 0, pa = 0;                         // blocks so far; a parity bit for each slot's cleaned uses
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
-      const AttnItem it = items[w / (2 * hk)];
-      const int n = key_blocks(it, w & 1, tok, causal);
+      const AttnItem it = items[w / (per * hk)];
+      const int n = key_blocks(it, w % per, tok, causal);
       if (n == 0) continue;
       na += (uint32_t)n;
       const int have = it.kn - (n - 1) * kAttnKeys;
@@ -746,7 +747,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
     if (!make_head_map(&mq, p, s.dtype, s.head_dim, 1, rows, stride, 1, kAttnKeys)) return cudaErrorInvalidValue;
     md = mk = mv = mq;
   }
-  const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * 2;
+  const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * a.l.tiles;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
