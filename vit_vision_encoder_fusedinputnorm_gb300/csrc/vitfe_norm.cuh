@@ -136,29 +136,35 @@ __device__ __forceinline__ void store_chunk(X* p, int i, int t, int width, const
   }
 }
 
-// A parameter vector as fp32 in shared memory, where every warp's chunk is a run of 8 or 16 bytes a
-// thread (no bank conflicts, no conversion and no type test for each row).
+// A vector as fp32 in shared memory, laid out so that every warp's chunk is a run of 8 or 16 bytes a
+// thread: no bank conflicts.  The place of column c:
+template <int V, int T, int C>
+__device__ __forceinline__ int staged_at(int c) {
+  using Ch = Chunks<V, T, C>;
+  int i, t, e;
+  if constexpr (V == 1) {
+    i = c / (2 * T);
+    e = c / T & 1;
+    t = c % T;
+  } else {
+    i = c / (T * V);
+    t = c / V % T;
+    e = c % V;
+  }
+  constexpr int W = Ch::E < 4 ? Ch::E : 4;     // floats of one access
+  return ((i * (Ch::E / W) + e / W) * T + t) * W + e % W;
+}
+
+// A parameter vector laid out so (no conversion and no type test for each row).
 template <int V, int T, int C>
 __device__ __forceinline__ void stage_params(float* dst, const void* p, vitfe_dtype d, float none, int width) {
-  using Ch = Chunks<V, T, C>;
   for (int c = threadIdx.x; c < C * T; c += kNormThreads) {
-    int i, t, e;
-    if constexpr (V == 1) {
-      i = c / (2 * T);
-      e = c / T & 1;
-      t = c % T;
-    } else {
-      i = c / (T * V);
-      t = c / V % T;
-      e = c % V;
-    }
     float f = none;
     if (p != nullptr && c < width)
       f = d == VITFE_F32    ? static_cast<const float*>(p)[c]
           : d == VITFE_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[c])
                             : to_f32(static_cast<const __half*>(p)[c]);
-    constexpr int W = Ch::E < 4 ? Ch::E : 4;     // floats of one access
-    dst[((i * (Ch::E / W) + e / W) * T + t) * W + e % W] = f;
+    dst[staged_at<V, T, C>(c)] = f;
   }
 }
 // (volatile, as the next one: the compiler would keep what it has read in registers, and spill)
@@ -382,26 +388,29 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + (int64_t)blockIdx.x * 2 * a.width;
-  float* part = reinterpret_cast<float*>(ring);      // [2][width]; the rows are done with
+  float* part = reinterpret_cast<float*>(ring);      // [2][C * T], staged; the rows are done with
+  constexpr int W = P < 2 ? P : 2;                    // pairs of one access
   __syncthreads();
   for (int j = 0; j < G; ++j) {                       // group after group: a fixed order of sums
     if (g == j) {
+      auto add = [&](float* to, const uint64_t (&v)[N][P]) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N; ++i) {
 #pragma unroll
-        for (int e = 0; e < Ch::E; ++e) {
-          const int c = Ch::col(i, t, e);
-          if (c >= width) continue;
-          const float vw = e & 1 ? hi_f32(dw[i][e / 2]) : lo_f32(dw[i][e / 2]);
-          const float vb = e & 1 ? hi_f32(db[i][e / 2]) : lo_f32(db[i][e / 2]);
-          part[c] = (j ? part[c] : 0.f) + vw;
-          part[a.width + c] = (j ? part[a.width + c] : 0.f) + vb;
+          for (int q = 0; q < P; q += W) {
+            uint64_t* at = reinterpret_cast<uint64_t*>(to) + ((i * (P / W) + q / W) * T + t) * W;
+#pragma unroll
+            for (int e = 0; e < W; ++e) at[e] = j ? add_f32x2(at[e], v[i][q + e]) : v[i][q + e];
+          }
         }
-      }
+      };
+      add(part, dw);
+      add(part + C * T, db);
     }
     __syncthreads();
   }
-  for (int c = threadIdx.x; c < 2 * a.width; c += kNormThreads) out[c] = part[c];
+  for (int c = threadIdx.x; c < 2 * a.width; c += kNormThreads)
+    out[c] = c < a.width ? part[staged_at<V, T, C>(c)] : part[C * T + staged_at<V, T, C>(c - a.width)];
 }
 
 // Whether every row and parameter vector starts on 16 bytes and holds a multiple of it.
@@ -444,7 +453,7 @@ cudaError_t launch_one(const NormArgs& a, cudaStream_t s) {
     int stages = (220 / backward_per_sm(C) * 1024 - fixed) / (G * 2 * slot);
     stages = stages > kNormStages ? kNormStages : stages < 1 ? 1 : stages;
     int smem = G * stages * 2 * slot;
-    if (smem < 2 * a.width * 4) smem = 2 * a.width * 4;
+    if (smem < 2 * C * T * (int)sizeof(float)) smem = 2 * C * T * (int)sizeof(float);
     smem += fixed;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<X, V, T, C>), 225 * 1024, allowed);
