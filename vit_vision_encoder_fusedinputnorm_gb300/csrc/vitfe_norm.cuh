@@ -426,7 +426,7 @@ bool rows_vec16(const NormArgs& a, bool backward) {
 
 // Blocks of the backward pass (one partial row of parameter sums each).
 int64_t backward_blocks(int64_t rows, int width) {
-  const int t = width <= 512 ? 32 : width <= 2048 ? 64 : width <= 4096 ? 128 : 256;
+  const int t = width <= 768 ? 32 : width <= 2048 ? 64 : width <= 4096 ? 128 : 256;
   const int64_t want = (rows + kNormThreads / t - 1) / (kNormThreads / t);
   const int64_t most = 152 * (width <= 256 ? 3 : width <= 8192 ? 2 : 1);
   return want < most ? (want > 0 ? want : 1) : most;
@@ -483,6 +483,7 @@ template <typename X, int V>
 cudaError_t launch_backward(const NormArgs& a, cudaStream_t s) {
   if (a.width <= 32 * 8) return launch_one<X, V, 32, 8, true>(a, s);
   if (a.width <= 32 * 16) return launch_one<X, V, 32, 16, true>(a, s);
+  if (a.width <= 32 * 24) return launch_one<X, V, 32, 24, true>(a, s);
   if (a.width <= 64 * 16) return launch_one<X, V, 64, 16, true>(a, s);
   if (a.width <= 64 * 24) return launch_one<X, V, 64, 24, true>(a, s);
   if (a.width <= 64 * 32) return launch_one<X, V, 64, 32, true>(a, s);
