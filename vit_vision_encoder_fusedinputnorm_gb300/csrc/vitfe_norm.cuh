@@ -20,9 +20,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// The lanes of a thread's group; a warp may hold several, each at a row of its own.
+template <int T>
+__device__ __forceinline__ unsigned group_lanes() {
+  if constexpr (T >= 32) return 0xffffffffu;
+  else return ((1u << T) - 1u) << (threadIdx.x & 31 & ~(T - 1));
+}
+
 template <int T>
 __device__ __forceinline__ void group_sync(int g) {
-  if constexpr (T == 32) __syncwarp();
+  if constexpr (T <= 32) __syncwarp(group_lanes<T>());
   else if constexpr (T == kNormThreads) __syncthreads();
   else named_bar_sync(1 + g, T);
 }
@@ -31,9 +38,9 @@ __device__ __forceinline__ void group_sync(int g) {
 template <int T, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float (*red)[kNormThreads / 32][2], int g, int& turn) {
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) {
+  for (int d = T < 32 ? T / 2 : 16; d >= 1; d >>= 1) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], d);
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(group_lanes<T>(), v[n], d);
   }
   if constexpr (T > 32) {
     constexpr int W = T / 32;
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
   using Ch = Chunks<V, T, C>;
   constexpr int N = Ch::N, P = Ch::P, G = kNormThreads / T;
   extern __shared__ __align__(16) char raw[];           // weight [C * T] fp32, then the ring
-  __shared__ uint64_t full[kNormThreads / 32][kNormStages];
+  __shared__ uint64_t full[G][kNormStages];
   __shared__ float red[2][kNormThreads / 32][2];
   __shared__ int abort_flag;
   const int t = threadIdx.x % T, g = threadIdx.x / T, width = a.width;
@@ -426,9 +433,9 @@ bool rows_vec16(const NormArgs& a, bool backward) {
 
 // Blocks of the backward pass (one partial row of parameter sums each).
 int64_t backward_blocks(int64_t rows, int width) {
-  const int t = width <= 768 ? 32 : width <= 2048 ? 64 : width <= 4096 ? 128 : 256;
+  const int t = width <= 128 ? 8 : width <= 256 ? 16 : width <= 768 ? 32 : width <= 2048 ? 64 : width <= 4096 ? 128 : 256;
   const int64_t want = (rows + kNormThreads / t - 1) / (kNormThreads / t);
-  const int64_t most = 152 * (width <= 256 ? 3 : width <= 8192 ? 2 : 1);
+  const int64_t most = 152 * (width <= 64 ? 3 : width <= 8192 ? 2 : 1);
   return want < most ? (want > 0 ? want : 1) : most;
 }
 
@@ -450,13 +457,13 @@ cudaError_t launch_one(const NormArgs& a, cudaStream_t s) {
     // beside the SM's other block
     const int slot = (a.width * (int)sizeof(X) + 30 + 15) / 16 * 16;
     const int fixed = C * T * (int)sizeof(float);
-    int stages = (220 / backward_per_sm(C) * 1024 - fixed) / (G * 2 * slot);
+    int stages = (216 / backward_per_sm(C) * 1024 - fixed) / (G * 2 * slot);
     stages = stages > kNormStages ? kNormStages : stages < 1 ? 1 : stages;
     int smem = G * stages * 2 * slot;
     if (smem < 2 * C * T * (int)sizeof(float)) smem = 2 * C * T * (int)sizeof(float);
     smem += fixed;
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<X, V, T, C>), 225 * 1024, allowed);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<X, V, T, C>), 222 * 1024, allowed);
     if (e != cudaSuccess) return e;
     norm_backward_kernel<X, V, T, C><<<(unsigned)backward_blocks(a.rows, a.width), kNormThreads, smem, s>>>(a, stages, slot);
     return cudaGetLastError();
@@ -468,7 +475,9 @@ cudaError_t launch_one(const NormArgs& a, cudaStream_t s) {
 template <typename X, int V>
 cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
   const int c = (a.width + 31) / 32;
-  if (c <= 8) return launch_one<X, V, 32, 8, false>(a, s);
+  if (a.width <= 64) return launch_one<X, V, 8, 8, false>(a, s);
+  if (a.width <= 128) return launch_one<X, V, 8, 16, false>(a, s);
+  if (a.width <= 256) return launch_one<X, V, 16, 16, false>(a, s);
   if (c <= 16) return launch_one<X, V, 32, 16, false>(a, s);
   if (c <= 24) return launch_one<X, V, 32, 24, false>(a, s);
   if (c <= 32) return launch_one<X, V, 32, 32, false>(a, s);
@@ -481,7 +490,9 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
 }
 template <typename X, int V>
 cudaError_t launch_backward(const NormArgs& a, cudaStream_t s) {
-  if (a.width <= 32 * 8) return launch_one<X, V, 32, 8, true>(a, s);
+  if (a.width <= 64) return launch_one<X, V, 8, 8, true>(a, s);
+  if (a.width <= 128) return launch_one<X, V, 8, 16, true>(a, s);
+  if (a.width <= 256) return launch_one<X, V, 16, 16, true>(a, s);
   if (a.width <= 32 * 16) return launch_one<X, V, 32, 16, true>(a, s);
   if (a.width <= 32 * 24) return launch_one<X, V, 32, 24, true>(a, s);
   if (a.width <= 64 * 16) return launch_one<X, V, 64, 16, true>(a, s);
