@@ -40,7 +40,7 @@ def _randn(seed, *shape, dtype=SF):
 
 NORM_SIZES = [(1, 1), (3, 7), (5, 33), (256, 1280), (70, 1152), (9, 80), (17, 2048), (4, 2056), (33, 1027), (2, 5000),
               (3, 8192), (2, 16384), (2, 16383), (1, 4100), (70, 64), (133, 100), (41, 128), (257, 200), (19, 256),
-              (700, 24), (50, 640)]
+              (700, 24), (50, 640), (6, 2700), (5, 3584)]
 
 
 def _norm_tol(x, mean, rstd, w, b, y):

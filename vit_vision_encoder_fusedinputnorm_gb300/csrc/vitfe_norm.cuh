@@ -225,10 +225,14 @@ __device__ __forceinline__ void load_staged(uint32_t src, int i, int t, int widt
   }
 }
 
+// Blocks of an SM: as many as the row's registers allow.  bf16: 589,824 x 1280 (40 columns a thread)
+// takes 521 us with four, which spill a few, and 486 with three; 589,824 x 640 (24) 242 and 266 us.
+__host__ __device__ constexpr int forward_per_sm(int C) { return C <= 24 ? 4 : C <= 40 ? 3 : 2; }
+
 // Forward: the row goes straight to registers (its threads' other rows cover the latency), the
 // mean and the squared deviations are two passes over them.
 template <typename X, int V, int T, int C>
-__global__ void __launch_bounds__(kNormThreads, (C <= 40 ? 4 : 2)) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, forward_per_sm(C)) norm_kernel(const NormArgs a) {
   using Ch = Chunks<V, T, C>;
   constexpr int N = Ch::N, P = Ch::P, G = kNormThreads / T;
   extern __shared__ __align__(16) float params[];      // [2][C * T]
@@ -443,7 +447,7 @@ template <typename X, int V, int T, int C, bool kBackward>
 cudaError_t launch_one(const NormArgs& a, cudaStream_t s) {
   constexpr int G = kNormThreads / T;
   if constexpr (!kBackward) {
-    const int64_t want = (a.rows + G - 1) / G, most = 152 * (T == 256 ? 1 : C <= 40 ? 4 : 2);
+    const int64_t want = (a.rows + G - 1) / G, most = 152 * (T == 256 ? 1 : forward_per_sm(C));
     const int smem = 2 * C * T * (int)sizeof(float);
     if (smem > 48 * 1024) {
       static std::atomic<uint64_t> allowed{0};
@@ -484,7 +488,9 @@ cudaError_t launch_forward(const NormArgs& a, cudaStream_t s) {
   if (c <= 40) return launch_one<X, V, 32, 40, false>(a, s);
   if (c <= 48) return launch_one<X, V, 32, 48, false>(a, s);
   if (c <= 64) return launch_one<X, V, 32, 64, false>(a, s);
-  if (a.width <= 128 * 32) return launch_one<X, V, 128, 32, false>(a, s);
+  if (a.width <= 64 * 40) return launch_one<X, V, 64, 40, false>(a, s);
+  if (a.width <= 64 * 48) return launch_one<X, V, 64, 48, false>(a, s);
+  if (a.width <= 64 * 64) return launch_one<X, V, 64, 64, false>(a, s);
   if (a.width <= 128 * 64) return launch_one<X, V, 128, 64, false>(a, s);
   return launch_one<X, V, 256, 64, false>(a, s);
 }
