@@ -289,6 +289,8 @@ vitfe_status vitfe_layer_norm(const void* x, int64_t x_row_stride, vitfe_dtype d
  * dout or x.  dweight, dbias: fp32 [width], either may be NULL; written, not
  * accumulated (0 for rows == 0).  The sums over rows are fp32 in a fixed order:
  * equal calls give equal bits.
+ * Rows of x and dout are read in whole aligned 16-byte words, each of which holds a
+ * byte of the row: up to 15 bytes on either side of it are read and not used.
  * workspace (16-byte aligned): vitfe_layer_norm_workspace(rows, width) bytes; may
  * be NULL when dweight and dbias are. */
 vitfe_status vitfe_layer_norm_backward(const void* dout, int64_t dout_row_stride, const void* x,

@@ -101,7 +101,8 @@ __device__ AttnKeyItem key_item(const PlanArgs& a, const int* scan, int n, int t
 // Tokens of a key item that see any of its keys.
 __device__ __forceinline__ int key_item_work(const AttnKeyItem& k) { return max(0, k.qn - max(0, -k.off)); }
 
-// One block: checks the boundaries, lists the query and key items of every sequence, cuts long
+// One block, since it is all latency (a dozen passes with a barrier each: 8 us for one sequence, 12 for
+// eight, 17 for 64 caches) and a plan serves every layer of a model.  It checks the boundaries, lists the query and key items of every sequence, cuts long
 // key ranges where there are few items, and sorts by length, longest first, so that the
 // attention kernels' fixed deal of items to SMs comes out even.  The order among equal
 // lengths may vary from call to call; no result depends on it.
@@ -235,9 +236,20 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
+// s = scale q.k over the keys that a row sees, p = exp(s - m) with a reference m of the row's, l = sum p,
+// out = (sum p v) / l, lse = m + log l; no key: 0 and -inf.  One pass over the keys: a block whose
+// largest score exceeds m by more than 8 (in powers of 2) moves m, and what has been summed is scaled;
+// below that p is at most 2^8, which fp32 sums and 16-bit p hold as well as 1.  s, p's sum and out's sums
+// are fp32; p is rounded to the tensors' type, as the tensor core takes it.
+//
 // One CTA per SM works through (item, key head) pairs.  An item has up to two score tiles of 128
 // rows (rows = tokens x the query heads of the key head, token-major), so that the tensor core
-// runs one tile's products while the other tile's probabilities are computed.
+// runs one tile's products while the other tile's probabilities are computed.  Heads of 128 come
+// near the tensor core's rate; below that a block's products are shorter than the way from scores to
+// probabilities and back (some 1400 cycles of each tile), which two tiles hide in part.  bf16: four
+// sequences of 9216, 16 heads of 80, 1.62 ms, 1.07 PFLOP/s, 55% of a dense product's rate; two of 8192,
+// 16 heads of 128, 0.73 ms, 78%; 16,384 causal, 0.71 ms, 80%; 64 tokens over 1..32,768 keys, 8 key heads
+// of 128, 155 us, 5.8 TB/s, 85% of what a copy reaches.
 //   warps 0-3, 4-7: softmax of tile 0, 1: thread = row.  Reads S from tensor memory, keeps the
 //     running maximum and sum in registers, writes P (16-bit) over S, rescales O when its
 //     reference maximum has to move, and stores the finished rows.
@@ -718,8 +730,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 // Joins the pieces of a cut item, in their order.  A piece holds its rows' maximum m (as an
 // exponent of 2), sum l and normalised output: out = sum of w_i out_i / sum of w_i,
-// w_i = l_i 2^(m_i - top).  (m and l
-// stay apart: m + log l would lose l next to a large score.)  A warp per row.
+// w_i = l_i 2^(m_i - top).  (m and l stay apart: m + log l would lose l next to a large score.)
+// A warp per row, its lanes over the pieces, then over the columns.  Latency: 64 tokens over 1..32,768
+// keys, 8 key heads of 128, 9.5 us alone; it is set up while the pieces end.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   grid_dep_wait();

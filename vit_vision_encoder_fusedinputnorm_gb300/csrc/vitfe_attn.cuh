@@ -80,7 +80,7 @@ inline AttnLayout attn_layout(const vitfe_attention_shape& s) {
   l.may_split = (s.rows_k + kAttnKeys - 1) / kAttnKeys > kAttnMinBlocks;
   const int64_t seqs = (int64_t)s.max_seqs + 1;
   // Pieces of items of many rows are as long as an SM's even share of the W blocks of all items and key
-  // heads, of few rows a sixth of it (attn_plan_kernel): at most `n` SM shares make n x SMs / heads
+  // heads, of few rows a fourth of it (attn_plan_kernel): at most `n` SM shares make n x SMs / heads
   // pieces beyond the first of each item, and twice that number of pieces in all.
   const int64_t many = l.may_split ? kAttnSMs / s.heads_kv + 1 : 0;
   const int64_t few = l.may_split ? kAttnFewCuts * kAttnSMs / s.heads_kv + 1 : 0;

@@ -4,6 +4,12 @@
 //   queries: dq of 128 rows, over the key blocks that they see (3 products a block).
 // S and dP are computed in both of the last two, so that every sum has one owner: no atomics, no
 // partial results, the same bits every time, for 7 products instead of 5.
+//   p = exp(s - lse), dp = dout.v, ds = p (dp - delta); dv = sum p dout, dk = scale sum ds q,
+//   dq = scale sum ds k; a key head's sums run over all its query heads.
+// s, dp and all sums are fp32, p and ds are rounded to the tensors' type, as the tensor core takes them.
+// bf16, eight sequences of 256 to 5184, 16 heads of 80: 24 + 505 + 446 us, 0.95 ms overlapped, 41% of a
+// dense product's rate counting five products (57% counting seven); two sequences of 8192, 16 heads of
+// 128: 2.5 ms, 56%.
 #include "vitfe_attn.cuh"
 
 namespace vitfe {
@@ -26,6 +32,8 @@ struct alignas(8) RowValue {
   float nlse2, ndelta;
 };
 
+// Memory bound: out and dout once.  Eight sequences of 256 to 5184, 16 heads of 80, in bf16 (92 MB):
+// 24 us, of which the bytes need 14; a fortieth of the whole.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const AttnArgs a) {
   grid_dep_trigger();
@@ -192,6 +200,9 @@ __device__ __forceinline__ TileRange query_tiles(const AttnKeyItem& it, int tok)
 // key), so that P^T and dS^T are A operands in tensor memory and Q and dO are read with their rows as the
 // contraction.  Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK: 128 columns each.
 // One matrix warp runs dV += P^T dO and the next S^T, the other dK += dS^T Q and the next dP^T.
+// Heads of 80: the score warps' way from S^T to dS^T bounds it (with nearly all of the products left out,
+// both kernels together still took 86% of their time); of 128: shared memory's bandwidth, which the
+// products' operands fill (with an eighth of the score products, 74%).
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -481,6 +492,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // dq.  Resident: the tiles of Q and dO.  Rings: K blocks and V blocks.  Lane = query row; four threads to
 // a row, 32 keys each.  Tensor memory: S (two buffers; dS over the one it came from), dP, dQ.
 // One matrix warp runs S and dP, the other dQ += dS K.
+// Bounded as the kernel above.
 // ---------------------------------------------------------------------------
 // Key blocks that tile t of an item reads, over the item's whole range (of a cut item the first
 // piece takes all of it: enough rows to fill the GPU are the rule in training).

@@ -24,7 +24,11 @@ __device__ __forceinline__ SpanScan scan_join(const SpanScan& a, const SpanScan&
   return SpanScan{a.tokens + b.tokens, b.restart ? b.reach : a.reach + b.reach, a.restart | b.restart};
 }
 
-// Every block scans the span table (it is small) and then places its own tokens.
+// A span is text, then a grid of t x h x w tokens (after merging) at position p = the text's end: token
+// (tg, y, x) of it has (p + tg step, p + y, p + x), and the next span begins one past the largest
+// position.  So a span's first position is a sum over those before it, back to the last restart: a
+// scan.  Every block scans the span table (it is small) and then places its own tokens: one launch,
+// no pass between the blocks.  Launch-bound: 5,000 rows take 3.7 us.
 __global__ void __launch_bounds__(kThreads) mrope_positions_kernel(
     const vitfe_span* __restrict__ spans, const int32_t* __restrict__ n_spans, int max_spans,
     const vitfe_item* __restrict__ items, const int32_t* __restrict__ n_items, int max_items, int merge, int rows,
@@ -152,9 +156,14 @@ struct MropeKernelArgs {
   long long x_stride[2], y_stride[2];
 };
 
+// (a, b) -> (a cos - b sin, b cos + a sin) for elements i and i + half of each head; `sign` turns back.
 // The angle of a pair is position * w_i.  In turns of 2^-64, position * turn[i] wraps as the
 // angle does, exactly, so no position loses accuracy: the phase's top 32 bits are the angle
 // to 2^-32 turns.
+// Memory bound (q and k, in and out).  A block makes the sines of its few rows once, in shared memory,
+// for all their heads, while the first rows' elements are on their way.  bf16, 32 + 8 heads of 128:
+// 16,384 rows 65 us, 5.2 TB/s, 76% of what a copy reaches; 65,536 rows 228 us, 87%; fp32, 16,384
+// rows 94%.  Blocks of twice or half the rows: 69 and 68 us; four rows in flight a thread: 95 us, spilled.
 template <typename X, int V>
 __global__ void __launch_bounds__(kThreads, 4) mrope_kernel(const __grid_constant__ MropeKernelArgs a, const __grid_constant__ MropeTable tab) {
   extern __shared__ __align__(16) float cs[];    // [rows_per_block][2][half]; half is a multiple of 4

@@ -1,4 +1,8 @@
-// Layer norm's kernels (memory bound: some ten operations an element, forward or backward).
+// Layer norm's kernels.  With xh = (x - mean) rstd, rstd = 1 / sqrt(mean((x - mean)^2) + eps):
+//   y = xh w + b
+//   g = dout w;  dx = rstd (g - mean(g) - xh mean(g xh));  dw = sum over rows of dout xh;  db = of dout
+// Some ten operations an element either way: memory bound.  All of it is held in fp32, and what is
+// stored in fewer bits is rounded once.
 //
 // A group of T threads holds one row: each thread owns at most 64 of its columns, so the row's
 // statistics are passes over registers, and the weight's gradient is summed in registers over all
@@ -229,8 +233,11 @@ __device__ __forceinline__ void load_staged(uint32_t src, int i, int t, int widt
 // takes 521 us with four, which spill a few, and 486 with three; 589,824 x 640 (24) 242 and 266 us.
 __host__ __device__ constexpr int forward_per_sm(int C) { return C <= 24 ? 4 : C <= 40 ? 3 : 2; }
 
-// Forward: the row goes straight to registers (its threads' other rows cover the latency), the
-// mean and the squared deviations are two passes over them.
+// Forward: the row goes straight to registers (the SM's other rows cover the latency), the mean and the
+// squared deviations are two passes over them: one read and one write of memory, and no cancellation.
+// bf16, 589,824 x 1280: 486 us, 6.2 TB/s, 92% of what a copy reaches; 18,048 x 1280: 20 us.  A ring of
+// bulk copies as the backward pass has took 986 us where this form took 584: the reads of shared
+// memory come on top, and the registers it frees are of no use here.
 template <typename X, int V, int T, int C>
 __global__ void __launch_bounds__(kNormThreads, forward_per_sm(C)) norm_kernel(const NormArgs a) {
   using Ch = Chunks<V, T, C>;
@@ -299,6 +306,10 @@ __host__ __device__ constexpr int backward_per_sm(int C) { return C <= 8 ? 3 : C
 // group's first thread keeps `stages` rows ahead (registers hold the parameter sums, not rows in
 // flight), and are read twice: for the sums, then for
 //   dx = dout (rstd w) + x A + B,  A = -rstd^2 mean(g xh),  B = -A mean - rstd mean(g).
+// Each block leaves one row of parameter sums, in a fixed order: no atomics, the same bits every time.
+// bf16, 589,824 x 1280: 685 us, 6.6 TB/s, 98% of what a copy reaches.  18,048 x 1280: 37 us where the
+// bytes need 20: the start, the blocks' sums and the kernel that adds them are some 17 us of it,
+// whatever the rows (9 us where only dx is asked for).
 template <typename X, int V, int T, int C>
 __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backward_kernel(const NormArgs a, int stages,
                                                                                        int slot) {

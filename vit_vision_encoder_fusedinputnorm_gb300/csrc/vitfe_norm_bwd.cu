@@ -4,7 +4,9 @@
 namespace vitfe {
 namespace {
 
-// Sum of the blocks' partial rows, [2][width] each: 32 columns by 32 slices of the rows a block.
+// Sum of the blocks' partial rows, [2][width] each: 32 columns by 32 slices of the rows a block, so
+// that few loads follow one another (304 rows of 2 x 1280: 4.5 us, latency; set up while the
+// kernel before it runs).
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restrict__ partial, int blocks, int width,
                                                            float* __restrict__ dweight, float* __restrict__ dbias) {
   __shared__ float red[32][33];
