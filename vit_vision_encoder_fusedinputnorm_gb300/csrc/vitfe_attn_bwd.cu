@@ -76,7 +76,7 @@ struct BwdShared {
   uint64_t a_full[kMaxSlots], a_empty[kMaxSlots], b_full[kMaxSlots], b_empty[kMaxSlots];
   uint64_t a_landed[kMaxSlots], b_landed[kMaxSlots];  // of tiles that are cleaned before they are full
   uint64_t row_full[kRowSlots], row_empty[kRowSlots];
-  uint64_t s_full[2], s_empty[2], dp_full, p_full, ds_full, acc_full, drain[2];
+  uint64_t s_full[2], s_empty[2], dp_full, dp_read, p_full, ds_full[2], acc_full, drain[2];
   uint32_t tmem;
   int abort;
   alignas(16) float nlse2[kRowSlots][kAttnRows], ndelta[kRowSlots][kAttnRows];   // of a query tile's rows
@@ -109,11 +109,12 @@ __device__ __forceinline__ void bwd_init(BwdShared& sh, uint32_t kv_users, uint3
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s_full[i]), 1);
       mbar_init(smem_u32(&sh.s_empty[i]), 1);
+      mbar_init(smem_u32(&sh.ds_full[i]), kScoreWarps);
       mbar_init(smem_u32(&sh.drain[i]), 1);
     }
     mbar_init(smem_u32(&sh.dp_full), 1);
     mbar_init(smem_u32(&sh.p_full), kScoreWarps);
-    mbar_init(smem_u32(&sh.ds_full), kScoreWarps);
+    mbar_init(smem_u32(&sh.dp_read), kScoreWarps);
     mbar_init(smem_u32(&sh.acc_full), acc_users);
     sh.abort = 0;
     fence_mbar_init();
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&sh.ds_full));
+          mbar_arrive(smem_u32(&sh.ds_full[0]));
           mbar_arrive(smem_u32(&sh.row_empty[stg]));
         }
       }
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         } else {
           if (!wait(&sh.a_full[pa.i], pa.parity) || (more && !wait(&sh.b_full[nbp.i], nbp.parity)) ||
-              !wait(&sh.ds_full, i & 1u))
+              !wait(&sh.ds_full[0], i & 1u))
             break;
           tc_fence_after();
           if (elect_one()) {
@@ -491,7 +492,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------------------
 // dq.  Resident: the tiles of Q and dO.  Rings: K blocks and V blocks.  Lane = query row; four threads to
 // a row, 32 keys each.  Tensor memory: S (two buffers; dS over the one it came from), dP, dQ.
-// One matrix warp runs S and dP, the other dQ += dS K.
+// One matrix warp runs S and dP, the other dQ += dS K.  dP's place is free as soon as all score warps
+// have it in their registers, so the next block's dP is not kept waiting for this one's dS (three per
+// cent of the gradients).  dS has two barriers in turn, as the score warps may be a block ahead.
 // Bounded as the kernel above.
 // ---------------------------------------------------------------------------
 // Key blocks that tile t of an item reads, over the item's whole range (of a cut item the first
@@ -571,6 +574,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         tmem_ld_32x32b_x32(dp_col + lanes + 32u * part, dp);
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.dp_read));
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const uint64_t x = mul_f32x2(pair_of(s + e), add_f32x2(pair_of(dp + e), nd));
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.ds_full));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ds_full[i & 1u]));
       }
       if (!ok || (n > 0 && !wait(&sh.acc_full, acc++ & 1u))) break;
       tc_fence_after();
@@ -680,18 +686,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const RingPos na = pa.next(ring.a), nbp = pb.next(ring.b);
         if (first) {
           if (more) {
-            if (!s_of(na, i + 1) || !wait(&sh.b_full[nbp.i], nbp.parity) || !wait(&sh.ds_full, i & 1u)) break;
+            if (!s_of(na, i + 1) || !wait(&sh.b_full[nbp.i], nbp.parity) || !wait(&sh.dp_read, i & 1u)) break;
             tc_fence_after();
             dp_of(nbp);
           } else {
             // the next item's first dP waits for the scores of this one's last block, as any other
             if (elect_one()) umma_commit(smem_u32(&sh.kv_empty));
             __syncwarp();
-            if (!wait(&sh.ds_full, i & 1u)) break;
+            if (!wait(&sh.dp_read, i & 1u)) break;
             tc_fence_after();
           }
         } else {
-          if (!wait(&sh.a_full[pa.i], pa.parity) || !wait(&sh.ds_full, i & 1u)) break;
+          if (!wait(&sh.a_full[pa.i], pa.parity) || !wait(&sh.ds_full[i & 1u], (i >> 1) & 1u)) break;
           tc_fence_after();
           if (elect_one()) {
             issue_sum<32>(dq_col, tmem + (i & 1u) * 128u, k_rows + pa.i * tile_step, id_acc, j > 0);
