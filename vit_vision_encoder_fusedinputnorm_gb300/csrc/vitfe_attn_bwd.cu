@@ -7,7 +7,7 @@
 //   p = exp(s - lse), dp = dout.v, ds = p (dp - delta); dv = sum p dout, dk = scale sum ds q,
 //   dq = scale sum ds k; a key head's sums run over all its query heads.
 // s, dp and all sums are fp32, p and ds are rounded to the tensors' type, as the tensor core takes them.
-// bf16, eight sequences of 256 to 5184, 16 heads of 80: 24 + 505 + 446 us, 0.95 ms overlapped, 41% of a
+// bf16, eight sequences of 256 to 5184, 16 heads of 80: 24 + 500 + 440 us, 0.95 ms overlapped, 41% of a
 // dense product's rate counting five products (57% counting seven); two sequences of 8192, 16 heads of
 // 128: 2.5 ms, 56%.
 #include "vitfe_attn.cuh"
@@ -201,9 +201,9 @@ __device__ __forceinline__ TileRange query_tiles(const AttnKeyItem& it, int tok)
 // key), so that P^T and dS^T are A operands in tensor memory and Q and dO are read with their rows as the
 // contraction.  Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK: 128 columns each.
 // One matrix warp runs dV += P^T dO and the next S^T, the other dK += dS^T Q and the next dP^T.
-// Heads of 80: the score warps' way from S^T to dS^T bounds it (with nearly all of the products left out,
-// both kernels together still took 86% of their time); of 128: shared memory's bandwidth, which the
-// products' operands fill (with an eighth of the score products, 74%).
+// Heads of 80: the score warps' way from S^T to dS^T bounds it (1,280 of a step's 2,260 cycles are
+// products; with nearly all of them left out, both kernels together still took 86% of their time); of
+// 128: the products (2,050 of 2,850 cycles).
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 1)
