@@ -537,3 +537,18 @@ def test_encoder_block_and_its_gradients():
 def test_example_runs():
     from vit_vision_encoder_fusedinputnorm_gb300 import block_example as X
     X.main()
+
+
+@pytest.mark.parametrize("lens", [[700, 300], [1] * 9 + [40], [5, 0, 1000]])
+def test_attention_plan_with_room_for_more_sequences(lens):
+    # the boundaries' capacity says nothing of how long the sequences are: the same bits either way
+    E = _enc()
+    rows, hq, hk, d = sum(lens), 4, 2, 80
+    q, k, v, do = (_randn(90 + i, rows, h, d, dtype=BF) for i, h in enumerate((hq, hk, hk, hq)))
+    results = []
+    for room in (0, 50):
+        cu = torch.tensor([0] + lens + [0] * room, device="cuda").cumsum(0).int()
+        plan = E.AttentionPlan(cu, cu, rows, rows, hq, hk, d, causal=True)
+        out, lse = E.attention(q, k, v, plan, lse=True)
+        results.append((out, lse) + E.attention_backward(do, q, k, v, out, lse, plan))
+    assert all(torch.equal(x, y) for x, y in zip(*results))

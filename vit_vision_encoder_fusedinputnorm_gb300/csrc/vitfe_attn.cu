@@ -106,12 +106,13 @@ __device__ __forceinline__ int key_item_work(const AttnKeyItem& k) { return max(
 // key ranges where there are few items, and sorts by length, longest first, so that the
 // attention kernels' fixed deal of items to SMs comes out even.  The order among equal
 // lengths may vary from call to call; no result depends on it.
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PlanArgs a) {
   __shared__ int warp_sums[32];
   __shared__ int bins[kBins];
   __shared__ unsigned bad;
   __shared__ unsigned long long blocks_total;
   __shared__ int slots[2], joins;            // of items of many and of few rows
+  __shared__ int live;                       // sequences with tokens
   const int tid = threadIdx.x;
   AttnPlanHdr* hdr = reinterpret_cast<AttnPlanHdr*>(a.plan);
   AttnItem* items = reinterpret_cast<AttnItem*>(a.plan + a.l.at_items);
@@ -122,13 +123,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   if (tid == 0) {
     bad = 0xffffffffu;
     blocks_total = 0;
-    slots[0] = joins = 0;
+    slots[0] = joins = live = 0;
     slots[1] = (int)a.l.cap_many;
   }
   __syncthreads();
   int n = a.max_seqs;
   for (int s = tid; s < n; s += kPlanThreads) {
     const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
+    if (q1 > q0) atomicAdd(&live, 1);
     if ((s == 0 && (q0 != 0 || k0 != 0)) || q0 < 0 || k0 < 0 || q1 < q0 || k1 < k0 || q1 > a.rows_q || k1 > a.rows_k) atomicMin(&bad, (unsigned)s);
   }
   __syncthreads();
@@ -137,6 +139,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
     a.status[1] = bad == 0xffffffffu ? -1 : (int)bad;
   }
   if (bad != 0xffffffffu) n = 0;
+  // Two tiles share an item's keys.  Where the sequences have no more tokens than one tile on average
+  // (single tokens above all), the second one would stay empty: an item is one tile then, and the
+  // kernel works on two items at a time.  bf16, the two-tile item's time first: the 64-token batch below
+  // 200 -> 164 us, windows of 64 tokens 417 -> 270 us, one token over 32,768 keys 45.5 -> 40 us; but a
+  // sequence of 16,384 715 -> 888 us.
+  const bool single = a.l.may_single && n > 0 && a.cu_q[n] <= (long long)live * a.l.tok;
+  a.item_tok = (single ? 1 : 2) * a.l.tok;
   int nq = 0, nk = 0;
   for (int b = 0; b <= n; b += kPlanThreads) {
     const int s = b + tid;
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const PlanArgs 
   }
   if (tid == 0) {
     __threadfence_block();
-    *hdr = AttnPlanHdr{n_items, nk, joins, 0};
+    *hdr = AttnPlanHdr{n_items, nk, joins, single ? 1 : 2};
   }
 }
 
@@ -310,13 +319,10 @@ __device__ __forceinline__ void next_work(WorkStream& s, const AttnItem* items, 
   s.live = true;
 }
 
-// kSingle: items of one tile, and each of the two tiles works through items of its own.
+// kSingle: items of one tile (AttnPlanHdr::tiles), and each of the two tiles works through items of its own.
 template <typename T, bool kSingle>
-__global__ void __launch_bounds__(kFwdThreads, 1)
-    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                const __grid_constant__ CUtensorMap map_v, int stages) {
-  extern __shared__ uint8_t raw[];
-  __shared__ FwdShared sh;
+__device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& map_q, const CUtensorMap& map_k,
+                                          const CUtensorMap& map_v, int stages, uint8_t* raw, FwdShared& sh) {
   const uint32_t tiles = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = a.s.heads_kv, g = a.l.group, d = a.s.head_dim, tok = a.l.tok;
@@ -357,6 +363,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
   const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
   const int works = hdr->n_items * hk, workers = (kSingle ? 2 : 1) * (int)gridDim.x;
+  // (neighbours in the list are key heads of the same rows: an SM's two tiles read them together)
+  auto worker = [&](int t) { return kSingle ? 2 * (int)blockIdx.x + t : (int)blockIdx.x; };
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax and output
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + (uint32_t)t * 128u;
     const uint32_t o_col = tmem + lanes + 256u + (uint32_t)t * 128u;
-    const int tile = kSingle ? 0 : t, id = kSingle ? 2 * (int)blockIdx.x + t : (int)blockIdx.x;
+    const int tile = kSingle ? 0 : t, id = worker(t);
     const int my_tok = tile * tok + row / g, head_in = row % g;
     const float scale2 = a.scale * 1.4426950408889634f;      // exponents of 2
     const AttnSlots slots(a.s, a.l);
@@ -525,7 +533,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if constexpr (kSingle) {
         WorkStream s[2];
         auto begin = [&](int t) {      // the next work's Q and first K
-          next_work(s[t], items, works, hk, 2 * (int)blockIdx.x + t, workers, tok, causal);
+          next_work(s[t], items, works, hk, worker(t), workers, tok, causal);
           if (s[t].live) ok = load_q(s[t].it, s[t].kh, t) && load(&map_k, s[t].kh, s[t].it.k0 + s[t].it.kb * kAttnKeys);
         };
 #pragma unroll
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       WorkStream s[2];
       RingPos pos;
       auto begin = [&](int t) {
-        next_work(s[t], items, works, hk, 2 * (int)blockIdx.x + t, workers, tok, causal);
+        next_work(s[t], items, works, hk, worker(t), workers, tok, causal);
         s[t].n = uniform(s[t].n);
         s[t].live = uniform(s[t].live) != 0;
         if (s[t].live) {
@@ -728,6 +736,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
+// kMaySingle: the shape allows items of one tile, and the plan says whether they are.  (Both ways in one
+// kernel cost the two-tile one 2.5%, so shapes that need only that have a kernel of their own.)
+template <typename T, bool kMaySingle>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v, int stages) {
+  extern __shared__ uint8_t raw[];
+  __shared__ FwdShared sh;
+  if constexpr (kMaySingle) {
+    if (reinterpret_cast<const AttnPlanHdr*>(a.plan)->tiles == 1) {
+      attn_body<T, true>(a, map_q, map_k, map_v, stages, raw, sh);
+      return;
+    }
+  }
+  attn_body<T, false>(a, map_q, map_k, map_v, stages, raw, sh);
+}
+
 // Joins the pieces of a cut item, in their order.  A piece holds its rows' maximum m (as an
 // exponent of 2), sum l and normalised output: out = sum of w_i out_i / sum of w_i,
 // w_i = l_i 2^(m_i - top).  (m and l stay apart: m + log l would lose l next to a large score.)
@@ -784,7 +809,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   }
 }
 
-template <typename T, bool kSingle>
+template <typename T, bool kMaySingle>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   const vitfe_attention_shape& s = a.s;
   CUtensorMap mq, mk, mv;
@@ -804,10 +829,10 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   int sms = 0;
   cudaError_t e = current_sms(&sms);
   if (e == cudaSuccess)
-    e = allow_smem(reinterpret_cast<const void*>(attn_kernel<T, kSingle>), kSmemMax - (int)sizeof(FwdShared), allowed, kFwdRegs);
+    e = allow_smem(reinterpret_cast<const void*>(attn_kernel<T, kMaySingle>), kSmemMax - (int)sizeof(FwdShared), allowed, kFwdRegs);
   if (e != cudaSuccess) return e;
-  const int64_t work = (a.l.cap_items * s.heads_kv + (kSingle ? 1 : 0)) / (kSingle ? 2 : 1);
-  attn_kernel<T, kSingle><<<(unsigned)(work < sms ? work : sms), kFwdThreads, smem, st>>>(a, mq, mk, mv, stages);
+  const int64_t work = a.l.cap_items * s.heads_kv;
+  attn_kernel<T, kMaySingle><<<(unsigned)(work < sms ? work : sms), kFwdThreads, smem, st>>>(a, mq, mk, mv, stages);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.l.may_split) return e;
   cudaLaunchConfig_t cfg = {};
@@ -835,7 +860,7 @@ cudaError_t launch_attention_plan(const vitfe_attention_shape& s, const int32_t*
   a.max_seqs = s.max_seqs;
   a.heads_kv = s.heads_kv;
   a.group = a.l.group;
-  a.item_tok = a.l.tiles * a.l.tok;
+  a.item_tok = 2 * a.l.tok;
   a.causal = s.causal;
   a.plan = static_cast<char*>(plan);
   a.status = status;
@@ -848,7 +873,7 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
     if (a.status != nullptr) status_ok_kernel<<<1, 1, 0, st>>>(a.status);
     return cudaGetLastError();
   }
-  if (a.l.tiles == 1)
+  if (a.l.may_single)
     return a.s.dtype == VITFE_F16 ? launch_typed<__half, true>(a, st) : launch_typed<__nv_bfloat16, true>(a, st);
   return a.s.dtype == VITFE_F16 ? launch_typed<__half, false>(a, st) : launch_typed<__nv_bfloat16, false>(a, st);
 }

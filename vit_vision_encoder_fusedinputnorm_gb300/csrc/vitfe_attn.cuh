@@ -54,14 +54,14 @@ struct alignas(16) AttnPlanHdr {
   int n_items;
   int n_keys;
   int n_joins;
-  int pad;
+  int tiles;      // score tiles of an item: 2, or 1 where sequences are short
 };
 
 // Capacities and offsets of a plan, from the shape alone.
 struct AttnLayout {
   int group;              // query heads to a key head
   int tok;                // tokens of one score tile: 128 / group
-  int tiles;              // score tiles of an item: 2, or 1 where sequences are short (attn_layout)
+  bool may_single;        // items may turn out to be of one score tile (attn_plan_kernel)
   int64_t cap_items, cap_keys, cap_joins;
   int64_t cap_many, cap_few;   // slots of partial results of items of many and of few rows
   int64_t at_items, at_keys, at_joins, at_scan_q, at_scan_k, bytes;
@@ -72,11 +72,7 @@ inline AttnLayout attn_layout(const vitfe_attention_shape& s) {
   AttnLayout l;
   l.group = s.heads_q / s.heads_kv;
   l.tok = kAttnRows / l.group;
-  // Two tiles share an item's keys.  Where the sequences have no more tokens than one tile on average
-  // (single tokens above all), the second one would stay empty: an item is one tile then, and the
-  // kernel works on two items at a time.  In bf16, the two-tile item's time first: the single-token
-  // batch 200 -> 164 us, windows of 64 tokens 417 -> 270 us, one token over 32,768 keys 45.5 -> 40 us.
-  l.tiles = s.max_seqs > 0 && s.rows_q <= (int64_t)s.max_seqs * l.tok ? 1 : 2;
+  l.may_single = s.max_seqs > 0 && s.rows_q <= (int64_t)s.max_seqs * l.tok;
   l.may_split = (s.rows_k + kAttnKeys - 1) / kAttnKeys > kAttnMinBlocks;
   const int64_t seqs = (int64_t)s.max_seqs + 1;
   // Pieces of items of many rows are as long as an SM's even share of the W blocks of all items and key
@@ -87,7 +83,7 @@ inline AttnLayout attn_layout(const vitfe_attention_shape& s) {
   l.cap_many = 2 * many;
   l.cap_few = 2 * few;
   auto lesser = [](int64_t a, int64_t b) { return a < b ? a : b; };
-  l.cap_items = s.rows_q / (l.tiles * l.tok) + lesser(seqs, s.rows_q) + many + few;
+  l.cap_items = s.rows_q / ((l.may_single ? 1 : 2) * l.tok) + lesser(seqs, s.rows_q) + many + few;
   l.cap_keys = s.rows_k / kAttnKeys + lesser(seqs, s.rows_k);
   l.cap_joins = many + few;
   int64_t at = sizeof(AttnPlanHdr);
@@ -107,7 +103,7 @@ inline AttnLayout attn_layout(const vitfe_attention_shape& s) {
 
 // Rows of a slot of an item of many rows.
 __host__ __device__ inline int64_t attn_slot_rows(const vitfe_attention_shape& s, const AttnLayout& l) {
-  return (s.rows_q < l.tiles * l.tok ? s.rows_q : l.tiles * l.tok) * l.group;
+  return (s.rows_q < 2 * l.tok ? s.rows_q : 2 * l.tok) * l.group;
 }
 // First row of a slot of one key head, in the workspace's [rows] of (maximum, sum) and of outputs; the
 // slots of an item's pieces follow each other heads_kv slots on.

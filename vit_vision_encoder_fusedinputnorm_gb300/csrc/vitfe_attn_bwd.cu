@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t dp_col = tmem + 256u, dq_col = tmem + 384u;    // S buffers: tmem, tmem + 128
   const AttnPlanHdr* hdr = reinterpret_cast<const AttnPlanHdr*>(a.plan);
   const AttnItem* items = reinterpret_cast<const AttnItem*>(a.plan + a.l.at_items);
-  const int per = a.l.tiles;                                    // score tiles of an item
+  const int per = hdr->tiles;                                   // score tiles of an item
   const int works = hdr->n_items * hk * per;                    // (item, key head, tile)
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {             // by a whole warp
@@ -765,7 +765,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
     if (!make_head_map(&mq, p, s.dtype, s.head_dim, 1, rows, stride, 1, kAttnKeys)) return cudaErrorInvalidValue;
     md = mk = mv = mq;
   }
-  const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * a.l.tiles;
+  const int64_t wk = a.l.cap_keys * s.heads_kv, wq = a.l.cap_items * s.heads_kv * 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
