@@ -24,6 +24,7 @@ constexpr int kBwdThreads = 32 * 20;
 constexpr int kMaxSlots = 4;         // of each ring
 constexpr int kRowSlots = 2;         // of the row values
 constexpr int kSmemMax = 227 * 1024;
+constexpr int kSharedFixed = 3 * 1024;      // BwdShared and what aligns the tiles behind it
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Per query row and head, negated: the log-sum-exp as an exponent of 2, and delta.  A row that sees
@@ -82,7 +83,7 @@ struct BwdShared {
   alignas(16) float nlse2[kRowSlots][kAttnRows], ndelta[kRowSlots][kAttnRows];   // of a query tile's rows
 };
 // With two column blocks to a tile, seven tiles and this fill an SM's shared memory to the byte.
-static_assert(sizeof(BwdShared) <= 3072, "");
+static_assert(sizeof(BwdShared) <= kSharedFixed, "");
 
 __device__ __forceinline__ int deal(int round) {
   return round * (int)gridDim.x + ((round & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
@@ -746,7 +747,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   const int64_t blocks = (s.rows_q * s.heads_q + 15) / 16;
   attn_rows_kernel<T><<<(unsigned)(blocks < 1 ? 1 : blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(a);
   const int tile = (s.head_dim + kColBlock - 1) / kColBlock * kColBlockBytes;
-  const uint32_t slots = (uint32_t)((kSmemMax - 3072) / tile - 2);
+  const uint32_t slots = (uint32_t)((kSmemMax - kSharedFixed) / tile - 2);
   RingSizes ring;
   ring.a = slots / 2 + (slots & 1u) < (uint32_t)kMaxSlots ? slots / 2 + (slots & 1u) : (uint32_t)kMaxSlots;
   ring.b = slots - ring.a < (uint32_t)kMaxSlots ? slots - ring.a : (uint32_t)kMaxSlots;
@@ -776,7 +777,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (s.rows_k > 0) {
-    e = allow_smem(reinterpret_cast<const void*>(attn_keys_kernel<T>), kSmemMax - 3072, allowed_keys);
+    e = allow_smem(reinterpret_cast<const void*>(attn_keys_kernel<T>), kSmemMax - kSharedFixed, allowed_keys);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(wk < sms ? wk : sms));
     e = cudaLaunchKernelEx(&cfg, attn_keys_kernel<T>, a, mq, md, mk, mv, ring);
@@ -785,7 +786,7 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t st) {
     cfg.numAttrs = 0;      // right behind the row values: it waits for them in full
   }
   if (s.rows_q > 0) {
-    e = allow_smem(reinterpret_cast<const void*>(attn_queries_kernel<T>), kSmemMax - 3072, allowed_queries);
+    e = allow_smem(reinterpret_cast<const void*>(attn_queries_kernel<T>), kSmemMax - kSharedFixed, allowed_queries);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(wq < sms ? wq : sms));
     e = cudaLaunchKernelEx(&cfg, attn_queries_kernel<T>, a, mq, md, mk, mv, ring);
