@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PlanArgs a) {
 // probabilities and back (some 1400 cycles of each tile), which two tiles hide in part.  bf16: four
 // sequences of 9216, 16 heads of 80, 1.62 ms, 1.07 PFLOP/s, 55% of a dense product's rate; two of 8192,
 // 16 heads of 128, 0.73 ms, 78%; 16,384 causal, 0.71 ms, 80%; 64 tokens over 1..32,768 keys, 8 key heads
-// of 128, 155 us, 5.8 TB/s, 85% of what a copy reaches.
+// of 128, 159 us, 5.6 TB/s, 83% of what a copy reaches.
 //   warps 0-3, 4-7: softmax of tile 0, 1: thread = row.  Reads S from tensor memory, keeps the
 //     running maximum and sum in registers, writes P (16-bit) over S, rescales O when its
 //     reference maximum has to move, and stores the finished rows.
