@@ -33,6 +33,14 @@ struct alignas(8) RowValue {
   float nlse2, ndelta;
 };
 
+// Read past L1, for a kernel that has not waited for the row values' kernel itself: that one has ended,
+// and its writes are in L2, before the kernel in between lets its successor start (it does so behind its own
+// wait); but an L1 may still hold what this workspace held in the call before.
+__device__ __forceinline__ RowValue row_value_l2(const RowValue* p) {
+  const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+  return RowValue{v.x, v.y};
+}
+
 // Memory bound: out and dout once.  Eight sequences of 256 to 5184, 16 heads of 80, in bf16 (92 MB):
 // 24 us, of which the bytes need 14; a fortieth of the whole.
 template <typename T>
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const bool live = row < tok * g && my_tok < it.qn;
       int lim = causal ? min(it.kn, it.off + my_tok + 1) : it.kn;
       RowValue v{-INFINITY, 0.f};
-      if (live) v = rows[((int64_t)it.q0 + my_tok) * a.s.heads_q + head];
+      if (live) v = row_value_l2(rows + ((int64_t)it.q0 + my_tok) * a.s.heads_q + head);
       else lim = 0;
       const uint64_t nl = f32x2(v.nlse2, v.nlse2), nd = f32x2(v.ndelta, v.ndelta);
       for (int j = 0; j < n; ++j, ++i) {
