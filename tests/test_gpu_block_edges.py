@@ -61,3 +61,53 @@ def test_attention_backward_takes_the_row_values_of_its_own_call():
     torch.cuda.synchronize()
     for r, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[r % 3])), r
+
+
+# ------------------------------------------------------------------ waits that run out
+
+EXPIRED = [6, -1]
+STALL_CASES = [  # lens_q, lens_k, q heads, k heads, head_dim, causal
+    ([300, 40], [300, 40], 2, 2, 80, False),                  # two-tile items
+    ([1] * 5, [1, 700, 2500, 129, 5000], 4, 2, 128, True),    # one-tile items, cut and joined
+]
+
+
+def _stall(monkeypatch, on):
+    if on:
+        monkeypatch.setenv("VITFE_WAIT_LIMIT_MS", "50")
+        monkeypatch.setenv("VITFE_TEST_STALL_BLOCK_LOADS", "1")
+    else:
+        monkeypatch.delenv("VITFE_WAIT_LIMIT_MS")
+        monkeypatch.delenv("VITFE_TEST_STALL_BLOCK_LOADS")
+
+
+def _stall_inputs(case):
+    E = _enc()
+    lq, lk, hq, hk, d, causal = case
+    plan = E.AttentionPlan(_cu(lq), _cu(lk), sum(lq), sum(lk), hq, hk, d, causal=causal)
+    q, do = (_randn(s, sum(lq), hq, d, dtype=BF) for s in (60, 61))
+    k, v = (_randn(s, sum(lk), hk, d, dtype=BF) for s in (62, 63))
+    return E, plan, q, k, v, do
+
+
+@pytest.mark.parametrize("case", STALL_CASES)
+def test_attention_reports_a_wait_that_runs_out_and_then_works_again(monkeypatch, case):
+    # tiles that never come: every role leaves by the short limit, and the context stays usable
+    E, plan, q, k, v, do = _stall_inputs(case)
+    st = torch.full((2,), -7, dtype=torch.int32, device="cuda")
+    want = E.attention(q, k, v, plan, lse=True)
+    grads = E.attention_backward(do, q, k, v, *want, plan)
+    _stall(monkeypatch, True)
+    E.attention(q, k, v, plan, status=st)
+    assert st.tolist() == EXPIRED
+    st.fill_(-7)
+    E.attention_backward(do, q, k, v, *want, plan, status=st)
+    assert st.tolist() == EXPIRED
+    _stall(monkeypatch, False)
+    got = E.attention(q, k, v, plan, lse=True, status=st)
+    assert st.tolist() == [0, -1]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    st.fill_(-7)
+    again = E.attention_backward(do, q, k, v, *want, plan, status=st)
+    assert st.tolist() == [0, -1]
+    assert all(torch.equal(a, b) for a, b in zip(again, grads))

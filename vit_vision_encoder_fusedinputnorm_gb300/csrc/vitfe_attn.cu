@@ -392,7 +392,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
       if (!live) lim = 0;
       float m = -INFINITY, l = 0.f;                          // m: the reference of the exponents
       for (int j = 0; j < n; ++j, ++ns) {
-        if (!wait_inline(&sh.s_full[t], ns & 1u, abort_flag)) {
+        if (!wait_inline(&sh.s_full[t], ns & 1u, abort_flag, a.wait_ns)) {
           ok = false;
           break;
         }
@@ -457,7 +457,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
       }
       if (!ok) break;
       if (n > 0) {
-        if (!wait_inline(&sh.o_full[t], no & 1u, abort_flag)) {
+        if (!wait_inline(&sh.o_full[t], no & 1u, abort_flag, a.wait_ns)) {
           ok = false;
           break;
         }
@@ -504,14 +504,14 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
   }
   if (warp == 8) {
     // ------------------------------------------------------------- loads
-    if (lane == 0) {
+    if (lane == 0 && !a.stall) {
       uint32_t nq[2] = {0, 0}, nk = 0;
       RingPos pos;
       bool ok = true;
       const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
       auto load = [&](const CUtensorMap* map, int head, int key) {
         const uint32_t st = pos.i;
-        if (!mbar_wait(smem_u32(&sh.kv_empty[st]), pos.parity ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        if (!mbar_wait(smem_u32(&sh.kv_empty[st]), pos.parity ^ 1u, abort_flag, a.wait_ns)) return false;
         pos = pos.next((uint32_t)stages);
         const uint32_t bar = smem_u32(&sh.kv_full[st]);
         mbar_arrive_expect_tx(bar, tile_bytes);
@@ -522,7 +522,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
       };
       auto load_q = [&](const AttnItem& it, int kh, int t) {
         const uint32_t bar = smem_u32(&sh.q_full[t]);
-        if (!mbar_wait(smem_u32(&sh.q_empty[t]), (nq[t] & 1u) ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        if (!mbar_wait(smem_u32(&sh.q_empty[t]), (nq[t] & 1u) ^ 1u, abort_flag, a.wait_ns)) return false;
         mbar_arrive_expect_tx(bar, q_bytes);
         for (int b = 0; b < nb; ++b)
           tma_load_3d(tiles + (uint32_t)t * tile_bytes + (uint32_t)b * kColBlockBytes, &map_q, bar, b * kColBlock,
@@ -571,12 +571,12 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
         const uint64_t t0 = global_timer_ns();
         for (int t = 0; t < 2; ++t)
           while (nq[t] > 0 && !mbar_try_wait(smem_u32(&sh.q_full[t]), (nq[t] - 1) & 1u) &&
-                 global_timer_ns() - t0 < kAttnWaitNs) {
+                 global_timer_ns() - t0 < kAttnDrainNs) {
           }
         const uint32_t back = nk < (uint32_t)stages ? nk : (uint32_t)stages;
         for (uint32_t i = nk - back; i < nk; ++i)
           while (!mbar_try_wait(smem_u32(&sh.kv_full[i % (uint32_t)stages]), (i / (uint32_t)stages) & 1u) &&
-                 global_timer_ns() - t0 < kAttnWaitNs) {
+                 global_timer_ns() - t0 < kAttnDrainNs) {
           }
       }
     }
@@ -593,7 +593,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
     RingPos kp, vp = kp.next(nst);                // the next K and V tile: K0 V0 K1 V1 ...
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && wait_inline(bar, parity, abort_flag);
+      ok = ok && wait_inline(bar, parity, abort_flag, a.wait_ns);
       return ok;
     };
     // S_t = Q_t K^T, announced on s_full; then `also` and `release`, when given
@@ -717,7 +717,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
     if (!ok) {      // matrix instructions in flight end on their own: wait for them
       if (elect_one()) umma_commit(smem_u32(&sh.drain));
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(smem_u32(&sh.drain), 0) && global_timer_ns() - t0 < kAttnWaitNs) {
+      while (!mbar_try_wait(smem_u32(&sh.drain), 0) && global_timer_ns() - t0 < kAttnDrainNs) {
       }
       __syncwarp();
     }

@@ -134,7 +134,7 @@ inline int64_t attn_backward_workspace(const vitfe_attention_shape& s) {
 // ---------------------------------------------------------------------------
 constexpr int kColBlock = 64;                             // 16-bit elements in one 128-byte row
 constexpr int kColBlockBytes = kAttnRows * 128;           // 128 rows of it
-constexpr uint64_t kAttnWaitNs = 1000000000ull;           // bound of every wait in the kernels
+constexpr uint64_t kAttnDrainNs = 1000000000ull;          // bound of the waits for what is in flight after an abort
 
 // Shared-memory descriptor of a tile of 128-byte rows (128-byte swizzle) read with the row index
 // as the contraction: 64 columns contiguous, 8 rows 1024 bytes apart, the next 64 columns one
@@ -258,13 +258,13 @@ __device__ __forceinline__ void issue_sum(uint32_t d_tmem, uint32_t a_tmem, uint
 }
 
 // mbar_wait_warp<false> all inline: a kernel that shares out its registers anew can hold no call.
-__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
   const uint32_t b = smem_u32(bar);
   if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 1;; ++i) {
     if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
-    if ((i & 15u) == 0 && __any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > kAttnWaitNs)) {
+    if ((i & 15u) == 0 && __any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > limit_ns)) {
       *abort_flag = 1;
       return false;
     }
@@ -300,6 +300,8 @@ struct AttnArgs {
   float* lse;
   void* workspace;
   int32_t* status;
+  uint64_t wait_ns;        // bound of every wait in the kernels
+  bool stall;              // tests: load nothing, so that the waits run out
   // backward
   const void* dout;
   void *dq, *dk, *dv;

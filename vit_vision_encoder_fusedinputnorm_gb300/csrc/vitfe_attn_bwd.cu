@@ -161,7 +161,7 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, uint32_t n, uint32_t
 __device__ __forceinline__ void drain_mma(uint64_t* bar) {
   if (elect_one()) umma_commit(smem_u32(bar));
   const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(smem_u32(bar), 0) && global_timer_ns() - t0 < kAttnWaitNs) {
+  while (!mbar_try_wait(smem_u32(bar), 0) && global_timer_ns() - t0 < kAttnDrainNs) {
   }
   __syncwarp();
 }
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int works = hdr->n_keys * hk;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {      // by a whole warp
-    ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
+    ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, a.wait_ns);
     return ok;
   };
 
@@ -338,13 +338,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_before();
     }
   } else if (warp == kLoadWarp) {
-    if (lane == 0) {
+    if (lane == 0 && !a.stall) {
       uint32_t la = 0, lb = 0, np = 0;      // loads into the rings and the resident tiles
       RingPos pa, pb;
       const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
       auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t base, RingPos& p, uint32_t slots,
                       uint32_t& count, int head, int row) {
-        if (!mbar_wait(smem_u32(&empty[p.i]), p.parity ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        if (!mbar_wait(smem_u32(&empty[p.i]), p.parity ^ 1u, abort_flag, a.wait_ns)) return false;
         mbar_arrive_expect_tx(smem_u32(&full[p.i]), q_bytes);
         load_tile(base + p.i * tile_bytes, map, smem_u32(&full[p.i]), nb, head, row);
         p = p.next(slots);
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int kh = w % hk;
         const TileRange tr = query_tiles(it, tok);
         if (tr.n == 0) continue;
-        if (!mbar_wait(smem_u32(&sh.kv_empty), (np & 1u) ^ 1u, abort_flag, kAttnWaitNs)) {
+        if (!mbar_wait(smem_u32(&sh.kv_empty), (np & 1u) ^ 1u, abort_flag, a.wait_ns)) {
           ok = false;
           break;
         }
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int works = hdr->n_items * hk * per;                    // (item, key head, tile)
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {             // by a whole warp
-    ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, kAttnWaitNs);
+    ok = ok && mbar_wait_warp<false>(smem_u32(bar), parity, abort_flag, a.wait_ns);
     return ok;
   };
 
@@ -614,13 +614,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_before();
     }
   } else if (warp == kLoadWarp) {
-    if (lane == 0) {
+    if (lane == 0 && !a.stall) {
       uint32_t la = 0, lb = 0, np = 0;      // loads into the rings and the resident tiles
       RingPos pa, pb;
       const uint32_t q_bytes = (uint32_t)(nb * tok * g) * 128u;
       auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, uint32_t base, RingPos& p, uint32_t slots,
                       uint32_t& count, int head, int key) {
-        if (!mbar_wait(smem_u32(&empty[p.i]), p.parity ^ 1u, abort_flag, kAttnWaitNs)) return false;
+        if (!mbar_wait(smem_u32(&empty[p.i]), p.parity ^ 1u, abort_flag, a.wait_ns)) return false;
         mbar_arrive_expect_tx(smem_u32(&full[p.i]), tile_bytes);
         load_tile(base + p.i * tile_bytes, map, smem_u32(&full[p.i]), nb, head, key);
         p = p.next(slots);
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int t = w % per, kh = w / per % hk;
         const int nk = key_blocks(it, t, tok, causal);
         if (nk == 0) continue;
-        if (!mbar_wait(smem_u32(&sh.kv_empty), (np & 1u) ^ 1u, abort_flag, kAttnWaitNs)) {
+        if (!mbar_wait(smem_u32(&sh.kv_empty), (np & 1u) ^ 1u, abort_flag, a.wait_ns)) {
           ok = false;
           break;
         }

@@ -79,6 +79,8 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// VITFE_TEST_STALL_BLOCK_LOADS=1: the kernels of this call issue no copies.
+bool stall_loads();
 // SMs of the current device, asked for once per device.
 cudaError_t current_sms(int* sms);
 // Allow `kernel` up to `smem` bytes of dynamic shared memory on the current device, once per device
@@ -108,6 +110,7 @@ struct NormArgs {
   float* dweight;
   float* dbias;
   float* partial;       // [CTA][2][width]
+  uint64_t wait_ns;     // bound of a wait
 };
 cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const NormArgs& a, cudaStream_t s);

@@ -1,5 +1,6 @@
 // C ABI of the encoder-block operators: argument validation, launches.
 #include <cmath>
+#include <cstdlib>
 
 #include "vitfe_attn.cuh"
 
@@ -113,6 +114,7 @@ vitfe_status vitfe_layer_norm_backward(const void* dout, int64_t dout_row_stride
   a.dweight = dweight;
   a.dbias = dbias;
   a.partial = params ? static_cast<float*>(workspace) : nullptr;
+  a.wait_ns = vitfe::wait_limit_ns();
   return from_cuda(vitfe::launch_layer_norm_backward(a, stream));
 }
 
@@ -228,6 +230,8 @@ vitfe_status vitfe_attention(const vitfe_attention_shape* shape, const void* pla
   a.lse = lse;
   a.workspace = workspace;
   a.status = status;
+  a.wait_ns = vitfe::wait_limit_ns();
+  a.stall = vitfe::stall_loads();
   return from_cuda(vitfe::launch_attention(a, stream));
 }
 
@@ -269,6 +273,8 @@ vitfe_status vitfe_attention_backward(const vitfe_attention_shape* shape, const 
   a.lse = const_cast<float*>(lse);
   a.workspace = workspace;
   a.status = status;
+  a.wait_ns = vitfe::wait_limit_ns();
+  a.stall = vitfe::stall_loads();
   a.dout = dout;
   a.dout_stride = dout_row_stride;
   a.dq = dq;
@@ -283,6 +289,11 @@ vitfe_status vitfe_attention_backward(const vitfe_attention_shape* shape, const 
 }  // extern "C"
 
 namespace vitfe {
+
+bool stall_loads() {
+  const char* env = std::getenv("VITFE_TEST_STALL_BLOCK_LOADS");
+  return env != nullptr && env[0] == '1';
+}
 
 cudaError_t current_sms(int* sms) {
   static std::atomic<int> known[64];

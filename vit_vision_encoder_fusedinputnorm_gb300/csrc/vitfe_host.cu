@@ -25,6 +25,14 @@ vitfe::EncodeTiledFn vitfe::encode_tiled_fn() {
   return fn;
 }
 
+uint64_t vitfe::wait_limit_ns() {
+  if (const char* env = std::getenv("VITFE_WAIT_LIMIT_MS")) {
+    const long ms = std::strtol(env, nullptr, 10);
+    if (ms > 0) return (uint64_t)ms * 1000000ull;
+  }
+  return 1000000000ull;
+}
+
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -189,10 +197,7 @@ vitfe_status vitfe_create(vitfe_t* out, const float mean[3], const float std_[3]
   c.kslice_pad = (c.kslice + 63) / 64 * 64;
   c.nblk = c.kslice_pad / 64;
   c.K = tpatch * c.kslice;
-  if (const char* env = std::getenv("VITFE_WAIT_LIMIT_MS")) {
-    const long ms = std::strtol(env, nullptr, 10);
-    if (ms > 0) c.wait_limit_ns = (uint64_t)ms * 1000000ull;
-  }
+  c.wait_limit_ns = vitfe::wait_limit_ns();
   if (const char* env = std::getenv("VITFE_TEST_STALL_W_LOADS")) c.test_stall_w_loads = env[0] == '1';
 
   if (cudaMalloc(&c.bias, (size_t)c.N * sizeof(float)) != cudaSuccess ||

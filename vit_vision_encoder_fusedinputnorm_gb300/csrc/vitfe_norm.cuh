@@ -16,7 +16,6 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormStages = 8;
-constexpr uint64_t kNormWaitNs = 1000000000ull;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
       rstd_next = __ldg(a.rstd + r + step);
     }
     // a bound on a wait for this group's own copy: a row that never came gives NaN
-    if (!mbar_wait(smem_u32(&full[g][st]), phase, &abort_flag, kNormWaitNs)) rstd = __int_as_float(0x7fffffff);
+    if (!mbar_wait(smem_u32(&full[g][st]), phase, &abort_flag, a.wait_ns)) rstd = __int_as_float(0x7fffffff);
     const uint32_t slot0 = smem_u32(mine + (size_t)st * 2 * slot) + (uint32_t)(t * V * (int)sizeof(X));
     const uint32_t x = slot0 + row_span(a.x, r, a.x_stride, width, sizeof(X)).skip;
     const uint32_t dy = slot0 + (uint32_t)slot + row_span(a.dout, r, a.dout_stride, width, sizeof(X)).skip;
