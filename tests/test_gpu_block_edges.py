@@ -111,3 +111,21 @@ def test_attention_reports_a_wait_that_runs_out_and_then_works_again(monkeypatch
     again = E.attention_backward(do, q, k, v, *want, plan, status=st)
     assert st.tolist() == [0, -1]
     assert all(torch.equal(a, b) for a, b in zip(again, grads))
+
+
+def test_attention_backward_on_a_long_stretch_of_whole_blocks(monkeypatch):
+    # eight sequences of whole key blocks before one that ends inside a block: nothing is cleaned for longer
+    # than the limit, which bounds one wait and not the call
+    E = _enc()
+    lens, h, d = [16384] * 8 + [100], 16, 64
+    rows = sum(lens)
+    q, k, v, do = (_randn(64 + i, rows, h, d, dtype=BF) for i in range(4))
+    plan = E.AttentionPlan(_cu(lens), _cu(lens), rows, rows, h, h, d)
+    out, lse = E.attention(q, k, v, plan, lse=True)
+    st = torch.full((2,), -7, dtype=torch.int32, device="cuda")
+    want = E.attention_backward(do, q, k, v, out, lse, plan, status=st)
+    assert st.tolist() == [0, -1]
+    monkeypatch.setenv("VITFE_WAIT_LIMIT_MS", "4")
+    got = E.attention_backward(do, q, k, v, out, lse, plan, status=st)
+    assert st.tolist() == [0, -1]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -88,6 +88,7 @@ struct BwdShared {
   uint64_t s_full[2], s_empty[2], dp_full, dp_read, p_full, ds_full[2], acc_full, drain[2];
   uint32_t tmem;
   int abort;
+  uint32_t loads;                                     // tiles asked for so far (query pass)
   alignas(16) float nlse2[kRowSlots][kAttnRows], ndelta[kRowSlots][kAttnRows];   // of a query tile's rows
 };
 // With two column blocks to a tile, seven tiles and this fill an SM's shared memory to the byte.
@@ -126,6 +127,7 @@ __device__ __forceinline__ void bwd_init(BwdShared& sh, uint32_t kv_users, uint3
     mbar_init(smem_u32(&sh.dp_read), kScoreWarps);
     mbar_init(smem_u32(&sh.acc_full), acc_users);
     sh.abort = 0;
+    sh.loads = 0;
     fence_mbar_init();
   }
   if ((threadIdx.x >> 5) == kMmaWarp) {
@@ -164,6 +166,27 @@ __device__ __forceinline__ void drain_mma(uint64_t* bar) {
   while (!mbar_try_wait(smem_u32(bar), 0) && global_timer_ns() - t0 < kAttnDrainNs) {
   }
   __syncwarp();
+}
+
+// A wait that may span works whose tiles are none of the waiter's: its bound counts from the last tile that
+// the loading warp has asked for (each of whose own waits is bounded).  By a whole warp.
+__device__ __forceinline__ bool wait_paced(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns,
+                                           const volatile uint32_t* loads) {
+  uint64_t t0 = global_timer_ns();
+  uint32_t seen = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_poll<false>(bar, parity))) return true;
+    if ((i & 15u) != 0) continue;
+    const uint32_t now = (uint32_t)uniform((int)*loads);
+    if (now != seen) {
+      seen = now;
+      t0 = global_timer_ns();
+    }
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > limit_ns)) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
 }
 
 // One tile's column blocks from a [rows][heads][head_dim] tensor.
@@ -625,6 +648,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         load_tile(base + p.i * tile_bytes, map, smem_u32(&full[p.i]), nb, head, key);
         p = p.next(slots);
         ++count;
+        *const_cast<volatile uint32_t*>(&sh.loads) = la + lb;
         return true;
       };
       for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
@@ -723,7 +747,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (!ok) drain_mma(&sh.drain[first ? 0 : 1]);
   } else {
     // K blocks that reach past their sequence: rows of others are zeroed for dQ (their dS is 0, but
-    // 0 * NaN is NaN)
+    // 0 * NaN is NaN).  Works that end with a whole block are passed over, so the wait for the next tile
+    // to clean may last as long as they do.
     uint32_t na = 0, pa = 0;                         // blocks so far; a parity bit for each slot's cleaned uses
     for (int r = 0, w = deal(0); ok && w < works; w = deal(++r)) {
       const AttnItem it = items[w / (per * hk)];
@@ -733,7 +758,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int have = it.kn - (n - 1) * kAttnKeys;
       if (have >= kAttnKeys) continue;
       const uint32_t sa = (na - 1u) % ring.a;
-      if (!wait(&sh.a_landed[sa], (pa >> sa) & 1u)) break;
+      if (!wait_paced(smem_u32(&sh.a_landed[sa]), (pa >> sa) & 1u, abort_flag, a.wait_ns, &sh.loads)) break;
       pa ^= 1u << sa;
       zero_tile_rows(ring_a + sa * tile_bytes, nb, have);
       if (lane == 0) mbar_arrive(smem_u32(&sh.a_full[sa]));
