@@ -393,7 +393,8 @@ vitfe_status vitfe_attention_plan(const vitfe_attention_shape* shape, const int3
  * probabilities are rounded to dtype for their product with V.
  * workspace: 16-byte aligned, vitfe_attention_workspace(shape) bytes (may be 0); one
  * call at a time may use it.  status (device int32[2]) or NULL: {0, -1}, or
- * {VITFE_EDEVICE_TIMEOUT, -1} when a bounded wait ran out (outputs invalid). */
+ * {VITFE_EDEVICE_TIMEOUT, -1} when a bounded wait ran out; outputs are invalid then,
+ * and the rows that were not written hold NaN. */
 int64_t vitfe_attention_workspace(const vitfe_attention_shape* shape);
 vitfe_status vitfe_attention(const vitfe_attention_shape* shape, const void* plan, const void* q,
                              int64_t q_row_stride, const void* k, int64_t k_row_stride,

@@ -98,11 +98,13 @@ def test_attention_reports_a_wait_that_runs_out_and_then_works_again(monkeypatch
     want = E.attention(q, k, v, plan, lse=True)
     grads = E.attention_backward(do, q, k, v, *want, plan)
     _stall(monkeypatch, True)
-    E.attention(q, k, v, plan, status=st)
+    missing = E.attention(q, k, v, plan, lse=True, status=st)
     assert st.tolist() == EXPIRED
     st.fill_(-7)
-    E.attention_backward(do, q, k, v, *want, plan, status=st)
+    missing += E.attention_backward(do, q, k, v, *want, plan, status=st)
     assert st.tolist() == EXPIRED
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), missing):      # nor does it take the status to see it
+        assert t.isnan().all(), name
     _stall(monkeypatch, False)
     got = E.attention(q, k, v, plan, lse=True, status=st)
     assert st.tolist() == [0, -1]

@@ -728,10 +728,23 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const CUtensorMap& 
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0 && a.status != nullptr) {
-    if (sh.abort) {
+  if (sh.abort) {
+    if (threadIdx.x == 0 && a.status != nullptr) {
       a.status[0] = kTimeout;
       a.status[1] = -1;
+    }
+    const AttnSlots slots(a.s, a.l);
+    for (int t = 0; t < (kSingle ? 2 : 1); ++t) {
+      for (int r = 0, w = deal(0, worker(t), workers); w < works; w = deal(++r, worker(t), workers)) {
+        const AttnItem it = items[w / hk];
+        const int kh = w % hk;
+        if (it.slot >= 0) {       // (a piece's sum: the join makes the rows of it)
+          fill_nan(static_cast<float*>(a.workspace) + 2 * slots.at(it.slot, kh), it.qn * g, 2, 2);
+        } else {
+          fill_nan(static_cast<T*>(a.out) + (int64_t)it.q0 * a.out_stride + kh * g * d, it.qn, a.out_stride, g * d);
+          if (a.lse) fill_nan(a.lse + (int64_t)it.q0 * a.s.heads_q + kh * g, it.qn, a.s.heads_q, g);
+        }
+      }
     }
   }
 }

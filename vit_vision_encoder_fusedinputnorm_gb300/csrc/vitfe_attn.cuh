@@ -283,6 +283,13 @@ __device__ __forceinline__ void zero_tile_rows(uint32_t tile, int blocks, int fi
   __syncwarp();
 }
 
+// After a wait that ran out, by the whole block: NaN over `n` rows of `len` elements (an item's: at
+// most 2^15), so that what is missing shows without the status as well.
+template <typename T>
+__device__ __forceinline__ void fill_nan(T* rows, int n, int64_t stride, int len) {
+  for (int i = threadIdx.x; i < n * len; i += blockDim.x) rows[i / len * stride + i % len] = from_f32<T>(NAN);
+}
+
 // Tensor map of a [rows][heads][head_dim] tensor; a box is 64 columns x box_heads x box_rows with
 // 128-byte swizzle, and what lies outside the tensor reads as zero.
 bool make_head_map(CUtensorMap* map, const void* p, vitfe_dtype dtype, int head_dim, int heads, int64_t rows,

@@ -519,6 +519,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   }
   bwd_end(sh, tmem, a.status);
+  for (int r = 0, w = deal(0); sh.abort && w < works; w = deal(++r)) {
+    const AttnKeyItem it = items[w / hk];
+    fill_nan(static_cast<T*>(a.dk) + (int64_t)it.k0 * a.dk_stride + w % hk * d, it.kn, a.dk_stride, d);
+    fill_nan(static_cast<T*>(a.dv) + (int64_t)it.k0 * a.dv_stride + w % hk * d, it.kn, a.dv_stride, d);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -768,6 +773,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // that what follows on the stream finds both done.
   grid_dep_wait();
   bwd_end(sh, tmem, a.status);
+  for (int r = 0, w = deal(0); sh.abort && w < works; w = deal(++r)) {
+    const AttnItem it = items[w / (per * hk)];
+    const int first = w % per * tok, n = it.kb > 0 ? 0 : min(tok, it.qn - first), head = w / per % hk * g;
+    fill_nan(static_cast<T*>(a.dq) + ((int64_t)it.q0 + first) * a.dq_stride + head * d, n, a.dq_stride, g * d);
+  }
 }
 
 template <typename T>
