@@ -43,7 +43,7 @@
  *    context stays usable.  VITFE_TEST_STALL_W_LOADS=1 at vitfe_create makes
  *    the embed kernel load no weights, to exercise that path in tests;
  *    VITFE_TEST_STALL_BLOCK_LOADS=1 at a call does so for the attention kernels'
- *    tiles.
+ *    tiles and the rows of the layer norm's gradients.
  *  - Bucket padding: rows at or past sum(t*h*w) up to `rows` are written as
  *    embedding 0, cos 1, sin 0, position id -1, flatten_patches 0.
  *  - Pixel reads: the library reads whole aligned words of 4, 8 or 16 bytes
@@ -293,6 +293,8 @@ vitfe_status vitfe_layer_norm(const void* x, int64_t x_row_stride, vitfe_dtype d
  * equal calls give equal bits.
  * Rows of x and dout are read in whole aligned 16-byte words, each of which holds a
  * byte of the row: up to 15 bytes on either side of it are read and not used.
+ * There is no status word: a row whose bounded wait ran out has NaN in dx, and
+ * dweight and dbias are NaN then.
  * workspace (16-byte aligned): vitfe_layer_norm_workspace(rows, width) bytes; may
  * be NULL when dweight and dbias are. */
 vitfe_status vitfe_layer_norm_backward(const void* dout, int64_t dout_row_stride, const void* x,

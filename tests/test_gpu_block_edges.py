@@ -131,3 +131,17 @@ def test_attention_backward_on_a_long_stretch_of_whole_blocks(monkeypatch):
     got = E.attention_backward(do, q, k, v, out, lse, plan, status=st)
     assert st.tolist() == [0, -1]
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,width", [(3, 100), (5000, 40), (4000, 1280), (700, 4000), (400, 9001)])
+def test_layer_norm_gradients_of_a_wait_that_runs_out_are_nan(monkeypatch, rows, width):
+    E = _enc()
+    x, dy, w = _randn(70, rows, width, dtype=BF), _randn(71, rows, width, dtype=BF), _randn(72, width)
+    _, mean, rstd = E.layer_norm(x, w, stats=True)
+    want = E.layer_norm_backward(dy, x, mean, rstd, w)
+    _stall(monkeypatch, True)
+    for t in E.layer_norm_backward(dy, x, mean, rstd, w):
+        assert t.isnan().all()
+    _stall(monkeypatch, False)
+    got = E.layer_norm_backward(dy, x, mean, rstd, w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

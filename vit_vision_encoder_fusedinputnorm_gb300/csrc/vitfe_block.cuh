@@ -111,6 +111,7 @@ struct NormArgs {
   float* dbias;
   float* partial;       // [CTA][2][width]
   uint64_t wait_ns;     // bound of a wait
+  bool stall;           // tests: load nothing, so that the waits run out
 };
 cudaError_t launch_layer_norm(const NormArgs& a, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(const NormArgs& a, cudaStream_t s);

@@ -115,6 +115,7 @@ vitfe_status vitfe_layer_norm_backward(const void* dout, int64_t dout_row_stride
   a.dbias = dbias;
   a.partial = params ? static_cast<float*>(workspace) : nullptr;
   a.wait_ns = vitfe::wait_limit_ns();
+  a.stall = vitfe::stall_loads();
   return from_cuda(vitfe::launch_layer_norm_backward(a, stream));
 }
 

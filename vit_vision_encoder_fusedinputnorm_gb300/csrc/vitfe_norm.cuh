@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
     bulk_load(dst, x.from, x.bytes, bar);
     bulk_load(dst + (uint32_t)slot, d.from, d.bytes, bar);
   };
-  if (t == 0)
+  if (t == 0 && !a.stall)
     for (int i = 0; i < stages && first + i * step < a.rows; ++i) fetch(first + i * step, i);
   stage_params<V, T, C>(weight, a.weight, a.param_dtype, 1.f, width);
   __syncthreads();
@@ -359,7 +359,8 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
       rstd_next = __ldg(a.rstd + r + step);
     }
     // a bound on a wait for this group's own copy: a row that never came gives NaN
-    if (!mbar_wait(smem_u32(&full[g][st]), phase, &abort_flag, a.wait_ns)) rstd = __int_as_float(0x7fffffff);
+    const bool here = mbar_wait(smem_u32(&full[g][st]), phase, &abort_flag, a.wait_ns);
+    if (!here) rstd = __int_as_float(0x7fffffff);
     const uint32_t slot0 = smem_u32(mine + (size_t)st * 2 * slot) + (uint32_t)(t * V * (int)sizeof(X));
     const uint32_t x = slot0 + row_span(a.x, r, a.x_stride, width, sizeof(X)).skip;
     const uint32_t dy = slot0 + (uint32_t)slot + row_span(a.dout, r, a.dout_stride, width, sizeof(X)).skip;
@@ -397,7 +398,8 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
       store_chunk<X, V, T, C>(dx, i, t, width, fx);
     }
     group_sync<T>(g);                         // the slot has been read
-    if (t == 0 && r + stages * step < a.rows) fetch(r + stages * step, st);
+    // (a slot whose copy did not come takes no other: its barrier still counts the first one)
+    if (t == 0 && here && r + stages * step < a.rows) fetch(r + stages * step, st);
     if (++st == stages) {
       st = 0;
       phase ^= 1u;
@@ -430,8 +432,10 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
     }
     __syncthreads();
   }
-  for (int c = threadIdx.x; c < 2 * a.width; c += kNormThreads)
-    out[c] = c < a.width ? part[staged_at<V, T, C>(c)] : part[C * T + staged_at<V, T, C>(c - a.width)];
+  for (int c = threadIdx.x; c < 2 * a.width; c += kNormThreads) {
+    const float sum = c < a.width ? part[staged_at<V, T, C>(c)] : part[C * T + staged_at<V, T, C>(c - a.width)];
+    out[c] = abort_flag ? __int_as_float(0x7fffffff) : sum;
+  }
 }
 
 // Whether every row and parameter vector starts on 16 bytes and holds a multiple of it.
