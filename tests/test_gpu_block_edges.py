@@ -145,3 +145,24 @@ def test_layer_norm_gradients_of_a_wait_that_runs_out_are_nan(monkeypatch, rows,
     _stall(monkeypatch, False)
     got = E.layer_norm_backward(dy, x, mean, rstd, w)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ layer norm far from zero
+
+@pytest.mark.parametrize("offset", [100.0, 1e4, -1e5])
+@pytest.mark.parametrize("rows,width", [(64, 1280), (40, 77), (9, 9000)])
+def test_layer_norm_gradients_of_rows_far_from_zero(rows, width, offset):
+    # the mean and rstd are given, so nothing of the offset may be left in the gradients.  Roundings, each E32
+    # of what it acts on: x - mean, xh, the products and at most 64 + 10 of a sum's additions (32 pairs of
+    # columns a thread and the exchanges) over magnitudes whose mean is at most their largest / 2; the rows'
+    # sums take at most 16 additions each (rows / groups) and 8 of the groups
+    E = _enc()
+    x, dy, w = _randn(80, rows, width) + offset, _randn(81, rows, width), _randn(82, width)
+    _, mean, rstd = E.layer_norm(x, w, stats=True)
+    dx, dw, db = E.layer_norm_backward(dy, x, mean, rstd, w)
+    rx, rdw, rdb, xh, g = R.layer_norm_backward(dy, x, mean, rstd, w)
+    top = g.abs().amax(1, keepdim=True)
+    mag = rstd.double()[:, None] * (g.abs() + top * (1 + xh.abs() * xh.abs().amax(1, keepdim=True)))
+    R.close(dx, rx, 48 * E32 * mag, "dx")
+    R.close(dw, rdw, 32 * E32 * (dy.double().abs() * xh.abs()).sum(0), "dweight")
+    R.close(db, rdb, 32 * E32 * dy.double().abs().sum(0), "dbias")
