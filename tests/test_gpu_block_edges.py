@@ -166,3 +166,17 @@ def test_layer_norm_gradients_of_rows_far_from_zero(rows, width, offset):
     R.close(dx, rx, 48 * E32 * mag, "dx")
     R.close(dw, rdw, 32 * E32 * (dy.double().abs() * xh.abs()).sum(0), "dweight")
     R.close(db, rdb, 32 * E32 * dy.double().abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("width", [41, 47, 896, 1280, 3584, 9001])
+def test_layer_norm_of_rows_of_equal_values_is_the_bias(width, dtype):
+    # values of few bits: their sum is exact, so the mean is the value and nothing deviates
+    E = _enc()
+    values = torch.tensor([0.0, 1.0, 3.0, 7.0, -5.0, 100.0, 1000.0, 200.0, -1.5], device="cuda")
+    x = values[:, None].expand(-1, width).contiguous().to(dtype)
+    w, b = _randn(83, width), _randn(84, width)
+    y, mean, rstd = E.layer_norm(x, w, b, 1e-6, stats=True)
+    assert torch.equal(mean, values)
+    assert torch.equal(y, b.to(dtype).expand(len(values), -1))
+    assert torch.equal(rstd, rstd[:1].expand(len(values))) and abs(float(rstd[0]) * 1e-3 - 1) <= 8 * E32 * 2

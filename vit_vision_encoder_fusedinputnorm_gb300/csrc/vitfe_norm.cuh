@@ -263,7 +263,9 @@ __global__ void __launch_bounds__(kNormThreads, forward_per_sm(C)) norm_kernel(c
     sum[0] = add_f32x2(sum[0], sum[1]);
     float m[1] = {lo_f32(sum[0]) + hi_f32(sum[0])};
     group_sum<T>(m, red, g, turn);
-    const float mean = m[0] * inv_n;
+    // a true division: 1 / width is rounded, and a row of equal values would deviate from its own mean by
+    // a unit of the last place, which rstd (up to 1 / sqrt(eps)) makes large
+    const float mean = m[0] / (float)width;
     const uint64_t minus = f32x2(-mean, -mean);
     uint64_t sq[2] = {0, 0};
 #pragma unroll
