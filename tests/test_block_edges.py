@@ -1,0 +1,32 @@
+"""Encoder-block operators, what the torch side has to see to itself (no GPU: the library's calls are
+stand-ins where one is reached)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from vit_vision_encoder_fusedinputnorm_gb300 import binding as B  # noqa: E402
+from vit_vision_encoder_fusedinputnorm_gb300 import encoder as E  # noqa: E402
+
+
+def test_the_table_rotation_refuses_other_types_and_tables(monkeypatch):
+    # the library's call takes addresses: it would turn any other type's bits as bfloat16
+    def never(*args):
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(B, "vitfe_rope_apply", never)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: pytest.MonkeyPatch.context())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: None)
+    x, cos = torch.zeros(4, 2, 16, dtype=torch.bfloat16), torch.zeros(4, 8)
+    for dtype in (torch.float16, torch.float32):
+        with pytest.raises(TypeError):
+            E.TableRotation.apply(x.to(dtype), cos, cos)
+        with pytest.raises(TypeError):
+            E.EncoderBlock(32, 2, 64, dtype=dtype, device="cpu")
+    for bad in (cos[:3], cos[:, :4], cos.double(), cos.bfloat16(), torch.zeros(8, 4).t(), torch.zeros(4, 16)[:, ::2], cos[0]):
+        with pytest.raises(ValueError):
+            E.TableRotation.apply(x, bad, cos)
+        with pytest.raises(ValueError):
+            E.TableRotation.apply(x, cos, bad)
+    with pytest.raises(ValueError):
+        E.TableRotation.apply(x[0], cos, cos)
+    with pytest.raises(ValueError):
+        E.TableRotation.apply(x, cos, cos)              # not on the GPU

@@ -375,10 +375,22 @@ class MropeRotation(torch.autograd.Function):
 
 
 class TableRotation(torch.autograd.Function):
-    """``TableRotation.apply(x, cos, sin)``: vitfe_rope_apply with the tower's tables, out of place."""
+    """``TableRotation.apply(x, cos, sin)``: vitfe_rope_apply with the tower's tables, out of place.
+
+    x: bfloat16 [rows][heads][head_dim]; cos, sin: float32 [rows][head_dim / 2].
+    """
 
     @staticmethod
     def _turn(x, cos, sin):
+        if x.dtype != torch.bfloat16:
+            raise TypeError(f"x: a bfloat16 tensor is needed, not {x.dtype}")
+        if x.dim() != 3:
+            raise ValueError(f"x: a [rows][heads][head_dim] tensor is needed, not {tuple(x.shape)}")
+        for t, name in ((cos, "cos"), (sin, "sin")):
+            if (t.dtype != _float32 or t.dim() != 2 or t.shape[0] < x.shape[0] or 2 * t.shape[1] != x.shape[2]
+                    or not t.is_contiguous()):
+                raise ValueError(f"{name}: a contiguous float32 {[x.shape[0], x.shape[2] // 2]} tensor is needed")
+        _device(x, cos, sin)
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device).copy_(x)
         with torch.cuda.device(x.device):
             B.vitfe_rope_apply(cos, sin, x.shape[0], x.shape[2], y, x.shape[1], _heads(y, "x"), None, 0, 0,
@@ -419,10 +431,13 @@ class EncoderBlock(torch.nn.Module):
     x + proj(attention(rotate(q), rotate(k), v)), then x + mlp: the rows are the front end's
     embeddings, cos and sin its RoPE tables, and the plan is made of its ``cu_seqlens``.  The
     projections are torch's matrix products; norms, rotation and attention are the library's.
+    In bfloat16, as the tower's rotation is.
     """
 
     def __init__(self, hidden: int, heads: int, mlp: int, eps: float = 1e-6, dtype=torch.bfloat16, device="cuda"):
         super().__init__()
+        if dtype != torch.bfloat16:
+            raise TypeError(f"the block is in bfloat16, not {dtype}")
         if hidden % heads or (hidden // heads) % 8:
             raise ValueError("hidden has to be heads times a multiple of 8")
         self.heads, self.eps = heads, eps
