@@ -30,3 +30,33 @@ def test_the_table_rotation_refuses_other_types_and_tables(monkeypatch):
         E.TableRotation.apply(x[0], cos, cos)
     with pytest.raises(ValueError):
         E.TableRotation.apply(x, cos, cos)              # not on the GPU
+
+
+class _Plan:
+    version = 1
+
+
+def _attention_stand_in(monkeypatch):
+    """attention and its gradients by torch, for one head and sequence."""
+    def forward(q, k, v, plan, scale=None, lse=False, **_):
+        s = (q[:, 0] @ k[:, 0].T) * (1.0 if scale is None else scale)
+        return (s.softmax(1) @ v[:, 0])[:, None], s.logsumexp(1)[:, None]
+
+    def backward(dout, q, k, v, out, lse, plan, scale=None, **_):
+        p = ((q[:, 0] @ k[:, 0].T) * (1.0 if scale is None else scale) - lse).exp()
+        ds = p * (dout[:, 0] @ v[:, 0].T - (dout * out)[:, 0].sum(1, keepdim=True)) * (1.0 if scale is None else scale)
+        return (ds @ k[:, 0])[:, None], (ds.T @ q[:, 0])[:, None], (p.T @ dout[:, 0])[:, None]
+    monkeypatch.setattr(E, "attention", forward)
+    monkeypatch.setattr(E, "attention_backward", backward)
+
+
+def test_gradients_across_an_update_of_the_plan_are_refused(monkeypatch):
+    _attention_stand_in(monkeypatch)
+    plan = _Plan()
+    q, k, v = (torch.randn(5, 1, 8, requires_grad=True) for _ in range(3))
+    E.PackedAttention.apply(q, k, v, plan, 0.3).sum().backward()
+    assert q.grad is not None
+    out = E.PackedAttention.apply(q, k, v, plan, 0.3)
+    plan.version += 1                                    # what update does
+    with pytest.raises(RuntimeError):
+        out.sum().backward()

@@ -180,3 +180,21 @@ def test_layer_norm_of_rows_of_equal_values_is_the_bias(width, dtype):
     assert torch.equal(mean, values)
     assert torch.equal(y, b.to(dtype).expand(len(values), -1))
     assert torch.equal(rstd, rstd[:1].expand(len(values))) and abs(float(rstd[0]) * 1e-3 - 1) <= 8 * E32 * 2
+
+
+# ------------------------------------------------------------------ plans and autograd
+
+def test_gradients_across_an_update_of_the_plan_are_refused():
+    E = _enc()
+    rows, h, d = 300, 2, 64
+    q, k, v = (_randn(90 + i, rows, h, d, dtype=BF).requires_grad_(True) for i in range(3))
+    plan = E.AttentionPlan(_cu([100, 200]), _cu([100, 200]), rows, rows, h, h, d)
+    out = E.PackedAttention.apply(q, k, v, plan, None)
+    plan.update(_cu([250, 50]), _cu([250, 50]))
+    with pytest.raises(RuntimeError):
+        out.float().sum().backward()
+    E.PackedAttention.apply(q, k, v, plan, None).float().sum().backward()
+    dout = torch.ones((rows, h, d), dtype=BF, device="cuda")
+    out, lse = E.attention(q.detach(), k.detach(), v.detach(), plan, lse=True)
+    for t, g in zip((q, k, v), E.attention_backward(dout, q.detach(), k.detach(), v.detach(), out, lse, plan)):
+        assert torch.equal(t.grad, g)

@@ -260,6 +260,7 @@ class AttentionPlan:
     def __init__(self, cu_q, cu_k, rows_q: int, rows_k: int, heads_q: int, heads_kv: int, head_dim: int,
                  causal: bool = False, status=None, stream=None):
         self.device = _device(cu_q, cu_k, status)
+        self.version = 0
         if cu_q.dim() != 1 or not len(cu_q):
             raise ValueError("cu_q: an int32 [sequences + 1] tensor is needed")
         shape = (rows_q, rows_k, len(cu_q) - 1, heads_q, heads_kv, head_dim, int(causal))
@@ -275,7 +276,11 @@ class AttentionPlan:
             self.update(cu_q, cu_k, status)
 
     def update(self, cu_q, cu_k, status=None, stream=None) -> None:
-        """Plan new boundaries in the same buffer (the shape stays: a captured graph replays this)."""
+        """Plan new boundaries in the same buffer (the shape stays: a captured graph replays this).
+
+        What was attended under the boundaries before keeps no copy of them: ``PackedAttention`` refuses
+        gradients across an update (``version`` counts them; a graph's replays are not seen).
+        """
         if stream is not None:
             with _current(stream):
                 return self.update(cu_q, cu_k, status)
@@ -283,6 +288,7 @@ class AttentionPlan:
         for c in (cu_q, cu_k):
             if c.dtype != torch.int32 or not c.is_contiguous() or c.shape != (self.shape.max_seqs + 1,):
                 raise ValueError(f"cu_q, cu_k: contiguous int32 [{self.shape.max_seqs + 1}] tensors are needed")
+        self.version += 1
         _launch("vitfe_attention_plan", device, self.shape, cu_q.data_ptr(), cu_k.data_ptr(), self.buffer.data_ptr(),
                 _ptr(status))
 
@@ -415,12 +421,14 @@ class PackedAttention(torch.autograd.Function):
     def forward(ctx, q, k, v, plan, scale):
         out, lse = attention(q, k, v, plan, scale, lse=True)
         ctx.save_for_backward(q, k, v, out, lse)
-        ctx.plan, ctx.scale = plan, scale
+        ctx.plan, ctx.scale, ctx.version = plan, scale, plan.version
         return out
 
     @staticmethod
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
+        if ctx.plan.version != ctx.version:
+            raise RuntimeError("the plan was updated since the forward pass: its gradients need the boundaries of then")
         dq, dk, dv = attention_backward(dout.contiguous(), q, k, v, out, lse, ctx.plan, ctx.scale)
         return dq, dk, dv, None, None
 
