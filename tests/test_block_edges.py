@@ -60,3 +60,34 @@ def test_gradients_across_an_update_of_the_plan_are_refused(monkeypatch):
     plan.version += 1                                    # what update does
     with pytest.raises(RuntimeError):
         out.sum().backward()
+
+
+def _all_functions(monkeypatch):
+    """Each autograd function over stand-ins: name -> a scalar of x."""
+    _attention_stand_in(monkeypatch)
+    monkeypatch.setattr(E, "layer_norm", lambda x, w, b, eps, stats: (x * w, x.mean(1), x.mean(1)))
+    monkeypatch.setattr(E, "layer_norm_backward", lambda dy, x, m, r, w, params: (dy * w, dy.sum(0), dy.sum(0)))
+    monkeypatch.setattr(E, "mrope_apply", lambda q, k, pos, axes, theta=1.0, inverse=False: tuple(
+        None if t is None else (-1 if inverse else 1) * t.flip(-1) for t in (q, k)))
+    monkeypatch.setattr(E.TableRotation, "_turn", staticmethod(lambda x, cos, sin: x * cos + x.flip(-1) * sin))
+    one, w, pos = torch.ones(4, 8), torch.ones(8), torch.zeros(3, 4, dtype=torch.int32)
+
+    def heads(x):
+        return x[:, None]
+    return {
+        "LayerNorm": lambda x: E.LayerNorm.apply(x, w, w, 1e-5),
+        "MropeRotation": lambda x: torch.cat(E.MropeRotation.apply(heads(x), heads(x), pos, [0] * 4, 10.0)),
+        "TableRotation": lambda x: E.TableRotation.apply(heads(x), one[:, None], one[:, None]),
+        "PackedAttention": lambda x: E.PackedAttention.apply(heads(x), heads(x), heads(x), _Plan(), 0.3),
+    }
+
+
+def test_gradients_of_gradients_are_refused(monkeypatch):
+    # backward's results carry no graph of their own: without a refusal its terms would be missing
+    for name, f in _all_functions(monkeypatch).items():
+        x = torch.randn(4, 8, requires_grad=True)
+        g, = torch.autograd.grad((f(x).square().sum() + x.pow(3).sum()), x, create_graph=True)
+        with pytest.raises(RuntimeError):
+            g.sum().backward()
+        f(x).square().sum().backward()                   # the first order is as it was
+        assert x.grad is not None, name

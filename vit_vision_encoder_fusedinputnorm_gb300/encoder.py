@@ -6,7 +6,7 @@ text, images and video.  PyTorch provides device memory and streams; every opera
 library's CUDA kernels (see ``binding``).
 
 The plain functions return gradients explicitly.  ``LayerNorm``, ``MropeRotation`` and
-``PackedAttention`` are the same calls as torch autograd functions, and ``EncoderBlock`` is a
+``PackedAttention`` are the same calls as torch autograd functions (of first order), and ``EncoderBlock`` is a
 pre-norm transformer block made of them.
 
 A call runs on the current stream, or on ``stream`` (a torch stream or a cudaStream_t), and what it
@@ -18,6 +18,7 @@ from __future__ import annotations
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -357,6 +358,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         params = ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
@@ -375,6 +377,7 @@ class MropeRotation(torch.autograd.Function):
         return mrope_apply(q, k, pos, axes, theta)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         dq, dk = mrope_apply(dq.contiguous(), dk.contiguous(), ctx.saved_tensors[0], ctx.axes, ctx.theta, inverse=True)
         return dq, dk, None, None, None
@@ -409,6 +412,7 @@ class TableRotation(torch.autograd.Function):
         return TableRotation._turn(x, cos, sin)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         cos, sin = ctx.saved_tensors
         return TableRotation._turn(dy, cos, -sin), None, None
@@ -425,6 +429,7 @@ class PackedAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
         if ctx.plan.version != ctx.version:
