@@ -91,3 +91,48 @@ def test_gradients_of_gradients_are_refused(monkeypatch):
             g.sum().backward()
         f(x).square().sum().backward()                   # the first order is as it was
         assert x.grad is not None, name
+
+
+class _Stream:
+    def __init__(self, device_index):
+        self.device_index = device_index
+
+
+def test_a_raw_stream_handle_is_one_of_the_tensors_gpu(monkeypatch):
+    # the tensors' GPU is 1, the current one is 0: the handle has to be made current on 1
+    made, launched = [], []
+
+    class Made:
+        def __init__(self, handle, device=None):
+            made.append((handle, device))
+
+        def __enter__(self):
+            return self
+
+        def __exit__(self, *_):
+            return False
+    monkeypatch.setattr(E, "_device", lambda *t: 1)
+    monkeypatch.setattr(torch.cuda, "Stream", _Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Made)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: 5)
+    monkeypatch.setattr(E, "_launch", lambda name, device, *a: launched.append((name, device)))
+    x, stat, pos = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4), torch.zeros(3, 4, dtype=torch.int32)
+    q, cu = x.view(4, 2, 8), torch.tensor([0, 4], dtype=torch.int32)
+    lse, one = torch.zeros(4, 2), torch.ones(1, dtype=torch.int32)
+    plan = E.AttentionPlan(cu, cu, 4, 4, 2, 2, 8, stream=77)
+    calls = [
+        lambda s: plan.update(cu, cu, stream=s),
+        lambda s: E.layer_norm(x, stream=s),
+        lambda s: E.layer_norm_backward(x, x, stat, stat, stream=s),
+        lambda s: E.mrope_positions(torch.zeros(1, 4, dtype=torch.int32), one, None, None, 4, stream=s),
+        lambda s: E.mrope_apply(None, q, pos, [0] * 4, stream=s),
+        lambda s: E.attention(q, q, q, plan, stream=s),
+        lambda s: E.attention_backward(q, q, q, q, q, lse, plan, stream=s),
+    ]
+    for f in calls:
+        f(77)
+    assert made == [(77, 1)] * (len(calls) + 1) and [d for _, d in launched] == [1] * (len(calls) + 1)
+    for f in calls:                                      # a stream of another GPU is an error
+        with pytest.raises(ValueError):
+            f(_Stream(0))

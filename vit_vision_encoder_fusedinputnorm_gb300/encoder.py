@@ -38,9 +38,14 @@ def _dtype(t: torch.Tensor) -> int:
     return code
 
 
-def _current(stream):
-    """Make ``stream`` current, so that outputs and workspaces are that stream's memory."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
+def _current(stream, x: torch.Tensor):
+    """Make ``stream`` current on x's GPU, so that outputs and workspaces are that stream's memory."""
+    device = _device(x)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)      # a handle does not say whose it is
+    elif stream.device_index != device:
+        raise ValueError(f"the stream is on GPU {stream.device_index}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _launch(name: str, device: int, *args) -> None:
@@ -118,7 +123,7 @@ def _vector(v: torch.Tensor, width: int, name: str, dtype: Optional[torch.dtype]
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stats: bool = False, stream=None):
     """Layer norm over the rows of x [rows][width]; with ``stats``: (y, mean, rstd) for the backward pass."""
     if stream is not None:
-        with _current(stream):
+        with _current(stream, x):
             return layer_norm(x, weight, bias, eps, out, stats)
     stride = _rows(x, "x")
     rows, width = x.shape
@@ -149,7 +154,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, stats: bo
 def layer_norm_backward(dout, x, mean, rstd, weight=None, params: bool = True, stream=None):
     """(dx, dweight, dbias) of layer_norm; the last two float32, or None without ``params``."""
     if stream is not None:
-        with _current(stream):
+        with _current(stream, x):
             return layer_norm_backward(dout, x, mean, rstd, weight, params)
     stride = _rows(x, "x")
     rows, width = x.shape
@@ -194,7 +199,7 @@ def mrope_positions(spans, n_spans, items, n_items, rows: int, merge: int = 2, p
     ``FrontEnd.upload`` (24 bytes an item), or None.
     """
     if stream is not None:
-        with _current(stream):
+        with _current(stream, spans):
             return mrope_positions(spans, n_spans, items, n_items, rows, merge, pos, status)
     device = _device(spans, n_spans, items, n_items, pos, status)
     if spans.dtype != torch.int32 or spans.dim() != 2 or spans.shape[1] != 4 or not spans.is_contiguous():
@@ -222,12 +227,12 @@ def mrope_apply(q, k, pos, axes: Sequence[int], theta: float = 10000.0, inverse:
     pos: int32 [n axes][rows]; axes: the axis of each pair (``section_axes``), rotary_dim / 2 of
     them.  q_out, k_out: where to write (q and k themselves for in place), else new tensors.
     """
-    if stream is not None:
-        with _current(stream):
-            return mrope_apply(q, k, pos, axes, theta, inverse, q_out, k_out)
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")
+    if stream is not None:
+        with _current(stream, x):
+            return mrope_apply(q, k, pos, axes, theta, inverse, q_out, k_out)
     device = _device(x, q, k, pos, q_out, k_out)
     if q is not None:
         q_out = _target(q, q_out, "q_out")
@@ -271,7 +276,7 @@ class AttentionPlan:
         self._q, self._k = (rows_q, heads_q, head_dim), (rows_k, heads_kv, head_dim)
         self._work = B.vitfe_attention_workspace(self.shape)
         self._work_backward = B.vitfe_attention_backward_workspace(self.shape)
-        with _current(stream if stream is not None else torch.cuda.current_stream(cu_q.device)):
+        with _current(stream if stream is not None else torch.cuda.current_stream(cu_q.device), cu_q):
             size = B.vitfe_attention_plan_bytes(self.shape)
             self.buffer = torch.empty(max(size, 16), dtype=torch.uint8, device=cu_q.device)
             self.update(cu_q, cu_k, status)
@@ -283,7 +288,7 @@ class AttentionPlan:
         gradients across an update (``version`` counts them; a graph's replays are not seen).
         """
         if stream is not None:
-            with _current(stream):
+            with _current(stream, cu_q):
                 return self.update(cu_q, cu_k, status)
         device = _device(self.buffer, cu_q, cu_k, status)
         for c in (cu_q, cu_k):
@@ -309,7 +314,7 @@ def attention(q, k, v, plan: AttentionPlan, scale: Optional[float] = None, lse: 
               stream=None):
     """softmax(scale q k^T) v over the plan's sequences; with ``lse``: (out, lse float32 [rows][heads])."""
     if stream is not None:
-        with _current(stream):
+        with _current(stream, q):
             return attention(q, k, v, plan, scale, lse, out, status)
     shape = plan.of(q, k, v)
     device = _device(plan.buffer, q, k, v, out, status)
@@ -326,7 +331,7 @@ def attention_backward(dout, q, k, v, out, lse, plan: AttentionPlan, scale: Opti
                        stream=None):
     """(dq, dk, dv) of attention; ``out`` and ``lse`` are the forward pass's."""
     if stream is not None:
-        with _current(stream):
+        with _current(stream, q):
             return attention_backward(dout, q, k, v, out, lse, plan, scale, status)
     shape = plan.of(q, k, v)
     device = _device(plan.buffer, dout, q, k, v, out, lse, status)
