@@ -136,3 +136,17 @@ def test_a_raw_stream_handle_is_one_of_the_tensors_gpu(monkeypatch):
     for f in calls:                                      # a stream of another GPU is an error
         with pytest.raises(ValueError):
             f(_Stream(0))
+
+
+@pytest.mark.parametrize("which", ["q", "k", "both"])
+def test_the_rotation_of_q_or_k_alone_has_a_gradient(monkeypatch, which):
+    _all_functions(monkeypatch)
+    pos = torch.zeros(3, 4, dtype=torch.int32)
+    q, k = (torch.randn(4, 1, 8, requires_grad=which in (n, "both")) if which in (n, "both") else None for n in "qk")
+    oq, ok = E.MropeRotation.apply(q, k, pos, [0] * 4, 10.0)
+    up = torch.randn(4, 1, 8)
+    sum((o * up).sum() for o in (oq, ok) if o is not None).backward()
+    for x, o in ((q, oq), (k, ok)):
+        assert (x is None) == (o is None)
+        if x is not None:
+            assert torch.equal(x.grad, -up.flip(-1))     # the stand-in's inverse

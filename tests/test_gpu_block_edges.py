@@ -198,3 +198,24 @@ def test_gradients_across_an_update_of_the_plan_are_refused():
     out, lse = E.attention(q.detach(), k.detach(), v.detach(), plan, lse=True)
     for t, g in zip((q, k, v), E.attention_backward(dout, q.detach(), k.detach(), v.detach(), out, lse, plan)):
         assert torch.equal(t.grad, g)
+
+
+@pytest.mark.parametrize("dtype", [BF, SF])
+@pytest.mark.parametrize("which", ["q", "k", "both"])
+def test_mrope_rotation_and_its_gradient(which, dtype):
+    E = _enc()
+    rows, d, axes = 21, 32, E.section_axes((6, 5, 5))
+    pos = torch.randint(0, 3000, (3, rows), generator=torch.Generator().manual_seed(1), dtype=torch.int32).cuda()
+    q = _randn(95, rows, 4, d, dtype=dtype).requires_grad_(True) if which != "k" else None
+    k = _randn(96, rows, 2, d, dtype=dtype).requires_grad_(True) if which != "q" else None
+    oq, ok = E.MropeRotation.apply(q, k, pos, axes, 1e4)
+    up = {2: _randn(97, rows, 2, d, dtype=dtype), 4: _randn(98, rows, 4, d, dtype=dtype)}
+    sum((o * up[o.shape[1]]).float().sum() for o in (oq, ok) if o is not None).backward()
+    for x, o in ((q, oq), (k, ok)):
+        if x is None:
+            assert o is None
+            continue
+        dx = up[o.shape[1]]
+        for got, ref in ((o, R.rotate(x.detach(), pos, axes, 1e4)), (x.grad, R.rotate(dx, pos, axes, 1e4, inverse=True))):
+            # angles to 2^-25 turns (float32 phases), then products in float32
+            R.close(got, ref, R.rounding(dtype, ref) + (8 * E32 + 2 * math.pi * 2.0 ** -25) * 2 * 5.0, "rotated")

@@ -373,7 +373,10 @@ class LayerNorm(torch.autograd.Function):
 
 
 class MropeRotation(torch.autograd.Function):
-    """``MropeRotation.apply(q, k, pos, axes, theta)``: mrope_apply; its gradient is the inverse rotation."""
+    """``MropeRotation.apply(q, k, pos, axes, theta)``: mrope_apply; its gradient is the inverse rotation.
+
+    q or k may be None, as there.
+    """
 
     @staticmethod
     def forward(ctx, q, k, pos, axes, theta):
@@ -384,7 +387,8 @@ class MropeRotation(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
-        dq, dk = mrope_apply(dq.contiguous(), dk.contiguous(), ctx.saved_tensors[0], ctx.axes, ctx.theta, inverse=True)
+        dq, dk = (None if g is None else g.contiguous() for g in (dq, dk))
+        dq, dk = mrope_apply(dq, dk, ctx.saved_tensors[0], ctx.axes, ctx.theta, inverse=True)
         return dq, dk, None, None, None
 
 
