@@ -1,5 +1,7 @@
 """Encoder-block operators, what the torch side has to see to itself (no GPU: the library's calls are
 stand-ins where one is reached)."""
+import contextlib
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -13,7 +15,7 @@ def test_the_table_rotation_refuses_other_types_and_tables(monkeypatch):
     def never(*args):
         raise AssertionError("the library was called")
     monkeypatch.setattr(B, "vitfe_rope_apply", never)
-    monkeypatch.setattr(torch.cuda, "device", lambda d: pytest.MonkeyPatch.context())
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d: None)
     x, cos = torch.zeros(4, 2, 16, dtype=torch.bfloat16), torch.zeros(4, 8)
     for dtype in (torch.float16, torch.float32):
@@ -150,3 +152,35 @@ def test_the_rotation_of_q_or_k_alone_has_a_gradient(monkeypatch, which):
         assert (x is None) == (o is None)
         if x is not None:
             assert torch.equal(x.grad, -up.flip(-1))     # the stand-in's inverse
+
+
+def test_status_pairs_and_counts_of_the_wrong_size_or_type_are_refused(monkeypatch):
+    # a kernel writes two words of status and reads one of a count, whatever the tensor holds
+    launched = []
+    monkeypatch.setattr(E, "_device", lambda *t: 1)
+    monkeypatch.setattr(E, "_current", lambda stream, x: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: 5)
+    monkeypatch.setattr(E, "_launch", lambda name, *a: launched.append(name))
+    x = torch.zeros(4, 2, 8, dtype=torch.bfloat16)
+    cu, lse, spans = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(4, 2), torch.zeros(1, 4, dtype=torch.int32)
+    one, good = torch.ones(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    plan = E.AttentionPlan(cu, cu, 4, 4, 2, 2, 8, status=good)
+    calls = [
+        lambda s: E.AttentionPlan(cu, cu, 4, 4, 2, 2, 8, status=s),
+        lambda s: plan.update(cu, cu, status=s),
+        lambda s: E.mrope_positions(spans, one, None, None, 4, status=s),
+        lambda s: E.attention(x, x, x, plan, status=s),
+        lambda s: E.attention_backward(x, x, x, x, x, lse, plan, status=s),
+    ]
+    for f in calls:
+        f(good)
+    del launched[:]
+    for bad in (one, good.long(), good.float(), torch.zeros(4, dtype=torch.int32)[::2]):
+        for f in calls:
+            with pytest.raises(ValueError):
+                f(bad)
+    none, items = torch.zeros(0, dtype=torch.int32), torch.zeros(24, dtype=torch.uint8)
+    for n, m in ((none, one), (one.long(), one), (one, none), (one, one.float())):
+        with pytest.raises(ValueError):
+            E.mrope_positions(spans, n, items, m, 4)
+    assert not launched

@@ -75,6 +75,15 @@ def _ptr(x: Optional[torch.Tensor]) -> Optional[int]:
     return None if x is None else x.data_ptr()
 
 
+def _words(t: Optional[torch.Tensor], count: int, name: str) -> Optional[int]:
+    """Address of `count` int32 that a kernel reads or writes, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() < count or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 [{count}] tensor is needed")
+    return t.data_ptr()
+
+
 def _rows(x: torch.Tensor, name: str) -> int:
     """Row stride of a [rows][width] tensor whose rows are contiguous."""
     if x.dim() != 2:
@@ -204,8 +213,6 @@ def mrope_positions(spans, n_spans, items, n_items, rows: int, merge: int = 2, p
     device = _device(spans, n_spans, items, n_items, pos, status)
     if spans.dtype != torch.int32 or spans.dim() != 2 or spans.shape[1] != 4 or not spans.is_contiguous():
         raise ValueError("spans: a contiguous int32 [capacity][4] tensor is needed")
-    if n_spans.dtype != torch.int32 or (n_items is not None and n_items.dtype != torch.int32):
-        raise ValueError("n_spans, n_items: int32 tensors are needed")
     capacity = 0
     if items is not None:
         if not items.is_contiguous():
@@ -215,8 +222,9 @@ def mrope_positions(spans, n_spans, items, n_items, rows: int, merge: int = 2, p
         pos = torch.empty((3, rows), dtype=torch.int32, device=spans.device)
     elif pos.shape != (3, rows) or pos.dtype != torch.int32 or not pos.is_contiguous():
         raise ValueError("pos: a contiguous int32 [3][rows] tensor is needed")
-    _launch("vitfe_mrope_positions", device, spans.data_ptr(), n_spans.data_ptr(), spans.shape[0], _ptr(items),
-            _ptr(n_items), capacity, merge, rows, pos.data_ptr(), _ptr(status))
+    _launch("vitfe_mrope_positions", device, spans.data_ptr(), _words(n_spans, 1, "n_spans"), spans.shape[0],
+            _ptr(items), _words(n_items, 1, "n_items"), capacity, merge, rows, pos.data_ptr(),
+            _words(status, 2, "status"))
     return pos
 
 
@@ -240,7 +248,7 @@ def mrope_apply(q, k, pos, axes: Sequence[int], theta: float = 10000.0, inverse:
     else:
         tq = (None, 0, 0, None, 0)
     if k is not None:
-        if k.dtype != x.dtype or k.shape[0] != x.shape[0] or k.shape[2] != x.shape[2]:
+        if k.dtype != x.dtype or k.dim() != 3 or k.shape[0] != x.shape[0] or k.shape[2] != x.shape[2]:
             raise ValueError("q and k: the same rows, head_dim and type are needed")
         k_out = _target(k, k_out, "k_out")
         tk = (k.data_ptr(), k.shape[1], _heads(k, "k"), k_out.data_ptr(), _heads(k_out, "k_out"))
@@ -294,9 +302,10 @@ class AttentionPlan:
         for c in (cu_q, cu_k):
             if c.dtype != torch.int32 or not c.is_contiguous() or c.shape != (self.shape.max_seqs + 1,):
                 raise ValueError(f"cu_q, cu_k: contiguous int32 [{self.shape.max_seqs + 1}] tensors are needed")
+        status = _words(status, 2, "status")
         self.version += 1
         _launch("vitfe_attention_plan", device, self.shape, cu_q.data_ptr(), cu_k.data_ptr(), self.buffer.data_ptr(),
-                _ptr(status))
+                status)
 
     def of(self, q, k, v) -> "B.AttentionShape":
         """The shape of a call with these tensors; raises where they do not fit the plan."""
@@ -323,7 +332,7 @@ def attention(q, k, v, plan: AttentionPlan, scale: Optional[float] = None, lse: 
     work = _empty(plan._work, dtype=torch.uint8, device=q.device) if plan._work else None
     _launch("vitfe_attention", device, shape, plan.buffer.data_ptr(), q.data_ptr(), _heads(q, "q"), k.data_ptr(),
             _heads(k, "k"), v.data_ptr(), _heads(v, "v"), q.shape[2] ** -0.5 if scale is None else scale,
-            out.data_ptr(), _heads(out, "out"), _ptr(sums), _ptr(work), _ptr(status))
+            out.data_ptr(), _heads(out, "out"), _ptr(sums), _ptr(work), _words(status, 2, "status"))
     return (out, sums) if lse else out
 
 
@@ -346,7 +355,7 @@ def attention_backward(dout, q, k, v, out, lse, plan: AttentionPlan, scale: Opti
             q.data_ptr(), _heads(q, "q"), k.data_ptr(), _heads(k, "k"), v.data_ptr(), _heads(v, "v"), out.data_ptr(),
             _heads(out, "out"), lse.data_ptr(), q.shape[2] ** -0.5 if scale is None else scale, dq.data_ptr(),
             _heads(dq, "dq"), dk.data_ptr(), _heads(dk, "dk"), dv.data_ptr(), _heads(dv, "dv"), _ptr(work),
-            _ptr(status))
+            _words(status, 2, "status"))
     return dq, dk, dv
 
 
