@@ -340,8 +340,9 @@ vitfe_status vitfe_mrope_positions(const vitfe_span* spans, const int32_t* n_spa
  * the head's first rotary_dim elements; the rest is copied.  inverse != 0 turns
  * the other way: the gradient of the call, and its undoing.
  * pos: device int32 [axes][rows]; axis_of_pair: HOST uint8 [rotary_dim / 2],
- * values below axes <= VITFE_MAX_AXES.  Angles are exact to 2^-32 turns at any
- * position (integer phases).  q: [rows][heads_q][head_dim] with a row stride,
+ * values below axes <= VITFE_MAX_AXES.  An angle is within 2^-26 turns (the phase as
+ * fp32) + |position| * 2^-53 turns (the frequency in 64 bits, theta >= 500), whatever
+ * the position: whole turns are dropped as integers.  q: [rows][heads_q][head_dim] with a row stride,
  * q_out likewise, and may be q; k, k_out likewise; heads_q or heads_k may be 0
  * (those pointers are then unused).  Bases 8-byte aligned (fp32: 16), strides
  * multiples of 4 elements.  head_dim % 8 == 0, rotary_dim % 8 == 0,

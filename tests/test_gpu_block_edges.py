@@ -219,3 +219,19 @@ def test_mrope_rotation_and_its_gradient(which, dtype):
         for got, ref in ((o, R.rotate(x.detach(), pos, axes, 1e4)), (x.grad, R.rotate(dx, pos, axes, 1e4, inverse=True))):
             # angles to 2^-25 turns (float32 phases), then products in float32
             R.close(got, ref, R.rounding(dtype, ref) + (8 * E32 + 2 * math.pi * 2.0 ** -25) * 2 * 5.0, "rotated")
+
+
+@pytest.mark.parametrize("theta", [500.0, 1e4, 1e6])
+@pytest.mark.parametrize("d", [64, 128, 512])
+def test_mrope_angles_are_within_the_stated_bound(theta, d):
+    # 2^-26 turns + position * 2^-53 turns; then a sine and a cosine (4 units), two products and a sum in float32,
+    # and the float64 reference's own angle (its product's rounding, half a unit of 2^-52, and its exponent's)
+    E = _enc()
+    pos = torch.tensor([[1, 1000, 32768, 10 ** 6, 8 * 10 ** 6 + 1, 10 ** 8, 2 ** 31 - 1, 2 ** 31 - 2]], dtype=torch.int32)
+    rows = pos.shape[1]
+    x = torch.zeros((rows, 1, d), device="cuda")
+    x[..., :d // 2] = 1.0                                # cos in the first half, sin in the second
+    y, _ = E.mrope_apply(x, None, pos.cuda(), [0] * (d // 2), theta=theta)
+    at = pos[0].double().cuda()[:, None, None]
+    tol = 2 * math.pi * (2.0 ** -26 + at * 2.0 ** -53) + 8 * E32 + at * 2.0 ** -50
+    R.close(y, R.rotate(x, pos, [0] * (d // 2), theta), tol, "angles")

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) mrope_positions_kernel(
 // rotation
 // ---------------------------------------------------------------------------
 struct MropeTable {
-  uint64_t turn[kMaxPairs];    // w_i / (2 pi) in units of 2^-64 turns
+  uint64_t turn[kMaxPairs];    // w_i / (2 pi) in units of 2^-64 turns, from 53-bit arithmetic
   uint8_t axis[kMaxPairs];
 };
 
@@ -158,8 +158,9 @@ struct MropeKernelArgs {
 
 // (a, b) -> (a cos - b sin, b cos + a sin) for elements i and i + half of each head; `sign` turns back.
 // The angle of a pair is position * w_i.  In turns of 2^-64, position * turn[i] wraps as the
-// angle does, exactly, so no position loses accuracy: the phase's top 32 bits are the angle
-// to 2^-32 turns.
+// angle does, so a position loses no more than it multiplies turn[i]'s own rounding by (2^-53 turns or
+// less for theta >= 500: products of doubles); the phase's top 32 bits become an fp32 number of half
+// turns, to 2^-25 of one.
 // Memory bound (q and k, in and out).  A block makes the sines of its few rows once, in shared memory,
 // for all their heads, while the first rows' elements are on their way.  bf16, 32 + 8 heads of 128:
 // 16,384 rows 65 us, 5.2 TB/s, 76% of what a copy reaches; 65,536 rows 228 us, 87%; fp32, 16,384
