@@ -1,6 +1,7 @@
 """Encoder-block operators, what the torch side has to see to itself (no GPU: the library's calls are
 stand-ins where one is reached)."""
 import contextlib
+import importlib.util
 
 import pytest
 
@@ -184,3 +185,13 @@ def test_status_pairs_and_counts_of_the_wrong_size_or_type_are_refused(monkeypat
         with pytest.raises(ValueError):
             E.mrope_positions(spans, n, items, m, 4)
     assert not launched
+
+
+def test_the_module_imports_under_a_torch_without_cuda(monkeypatch):
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name)
+    spec = importlib.util.spec_from_file_location(E.__name__ + "_again", E.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    with pytest.raises(ValueError):
+        again.layer_norm(torch.zeros(2, 8))              # not on a GPU

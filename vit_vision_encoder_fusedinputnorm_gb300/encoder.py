@@ -25,7 +25,8 @@ from . import binding as B
 _DTYPES = {torch.bfloat16: B.VITFE_BF16, torch.float16: B.VITFE_F16, torch.float32: B.VITFE_F32}
 _float32 = torch.float32
 _empty, _empty_like = torch.empty, torch.empty_like
-_get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# (a torch built without CUDA has neither, nor a tensor that a call would take)
+_get_device, _raw_stream = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
 
 # A call of these costs a few microseconds beside kernels that may take as few, so the helpers below
