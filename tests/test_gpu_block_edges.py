@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import block_reference as R  # noqa: E402
+import test_gpu_block_ops as T  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -218,7 +219,7 @@ def test_mrope_rotation_and_its_gradient(which, dtype):
         dx = up[o.shape[1]]
         for got, ref in ((o, R.rotate(x.detach(), pos, axes, 1e4)), (x.grad, R.rotate(dx, pos, axes, 1e4, inverse=True))):
             # angles to 2^-25 turns (float32 phases), then products in float32
-            R.close(got, ref, R.rounding(dtype, ref) + (8 * E32 + 2 * math.pi * 2.0 ** -25) * 2 * 5.0, "rotated")
+            R.close(got.detach(), ref, R.rounding(dtype, ref) + (8 * E32 + 2 * math.pi * 2.0 ** -25) * 2 * 5.0, "rotated")
 
 
 @pytest.mark.parametrize("theta", [500.0, 1e4, 1e6])
@@ -235,3 +236,185 @@ def test_mrope_angles_are_within_the_stated_bound(theta, d):
     at = pos[0].double().cuda()[:, None, None]
     tol = 2 * math.pi * (2.0 ** -26 + at * 2.0 ** -53) + 8 * E32 + at * 2.0 ** -50
     R.close(y, R.rotate(x, pos, [0] * (d // 2), theta), tol, "angles")
+
+
+# ------------------------------------------------------------------ layouts
+
+def _bytes_off(rows, width, pad, dtype, seed):
+    """[rows][width] inside wider rows, `pad` elements in."""
+    return _randn(seed, rows, width + pad + 9, dtype=dtype)[:, pad:pad + width]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("width,pads", [(1280, (0, 0)), (1280, (8, 3)), (1280, (1, 0)), (77, (2, 5)), (2049, (0, 7)),
+                                        (64, (8, 16)), (9000, (3, 4))])
+def test_layer_norm_gradients_of_rows_inside_wider_ones(width, pads, dtype):
+    # x and dout at different distances from 16 bytes, each: the same values as of dense rows
+    E = _enc()
+    rows = 29
+    x, dy = (_bytes_off(rows, width, p, dtype, 100 + i) for i, p in enumerate(pads))
+    w = _randn(102, width)
+    _, mean, rstd = E.layer_norm(x, w, stats=True)
+    dx, dw, db = E.layer_norm_backward(dy, x, mean, rstd, w)
+    rx, rdw, rdb, xh, g = R.layer_norm_backward(dy, x, mean, rstd, w)
+    top = g.abs().amax(1, keepdim=True)
+    mag = rstd.double()[:, None] * (g.abs() + top * (1 + xh.abs() * xh.abs().amax(1, keepdim=True)))
+    R.close(dx, rx, R.rounding(dtype, rx) + 48 * E32 * mag, "dx")          # roundings as of rows far from zero
+    R.close(dw, rdw, 32 * E32 * (dy.double().abs() * xh.abs()).sum(0), "dweight")
+    R.close(db, rdb, 32 * E32 * dy.double().abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("width", [1280, 77, 9000])
+@pytest.mark.parametrize("over", ["x", "dout"])
+def test_layer_norm_gradient_over_its_input(width, over):
+    from vit_vision_encoder_fusedinputnorm_gb300 import binding as B
+    E = _enc()
+    rows = 2000
+    x, dy, w = _randn(110, rows, width, dtype=BF), _randn(111, rows, width, dtype=BF), _randn(112, width)
+    _, mean, rstd = E.layer_norm(x, w, stats=True)
+    want = E.layer_norm_backward(dy, x, mean, rstd, w)
+    dx = x if over == "x" else dy
+    dw, db = torch.empty(width, device="cuda"), torch.empty(width, device="cuda")
+    size = B.vitfe_layer_norm_workspace(rows, width)
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    B.vitfe_layer_norm_backward(dy, width, x, width, B.VITFE_BF16, rows, width, w, B.VITFE_F32, mean, rstd, dx, width,
+                                dw, db, work, size, torch.cuda.current_stream())
+    assert all(torch.equal(a, b) for a, b in zip((dx, dw, db), want))
+
+
+@pytest.mark.parametrize("params", ["both", "weight", "bias", "none"])
+def test_layer_norm_function_with_and_without_parameters(params):
+    E = _enc()
+    x = _randn(115, 33, 96).requires_grad_(True)
+    w = _randn(116, 96, dtype=BF).requires_grad_(True) if params in ("both", "weight") else None
+    b = _randn(117, 96, dtype=BF).requires_grad_(True) if params in ("both", "bias") else None
+    up = _randn(118, 96, 33).t()                                # a gradient that is not contiguous
+    y = E.LayerNorm.apply(x, w, b, 1e-5)
+    y.backward(up)
+    _, mean, rstd = E.layer_norm(x.detach(), w, b, 1e-5, stats=True)
+    dx, dw, db = E.layer_norm_backward(up.contiguous(), x.detach(), mean, rstd, w)
+    assert torch.equal(x.grad, dx)
+    assert w is None or torch.equal(w.grad, dw.to(BF))
+    assert b is None or torch.equal(b.grad, db.to(BF))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("scale", [0.03, 0.4])
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_and_its_gradients_with_a_scale_and_rows_inside_wider_ones(causal, scale, dtype):
+    E = _enc()
+    lens, hq, hk, d = [130, 257, 1], 4, 2, 72
+    rows = sum(lens)
+
+    def wide(seed, h):
+        return _randn(seed, rows, h + 1, d, dtype=dtype)[:, 1:]
+    q, k, v, do = wide(120, hq), wide(121, hk), wide(122, hk), wide(123, hq)
+    plan = E.AttentionPlan(_cu(lens), _cu(lens), rows, rows, hq, hk, d, causal=causal)
+    out, lse = E.attention(q, k, v, plan, scale=scale, lse=True, out=wide(124, hq))
+    got = E.attention_backward(do, q, k, v, out, lse, plan, scale=scale)
+    r = R.attention(q, k, v, lens, lens, causal, scale=scale, dout=do, out=out)
+    err = T._score_error(r["score"], d)
+    T._close_rounded(out, r, "out", dtype, 2 * err)
+    for name, g in zip(("dq", "dk", "dv"), got):
+        T._close_rounded(g, r, name, dtype, 4 * err)
+
+
+def test_packed_attention_function_takes_a_scale_and_any_gradient():
+    E = _enc()
+    lens, h, d = [100, 60], 2, 64
+    rows = sum(lens)
+    q, k, v = (_randn(130 + i, rows, h, d, dtype=BF).requires_grad_(True) for i in range(3))
+    plan = E.AttentionPlan(_cu(lens), _cu(lens), rows, rows, h, h, d)
+    up = _randn(133, h, rows, d, dtype=BF).transpose(0, 1)
+    E.PackedAttention.apply(q, k, v, plan, 0.2).backward(up)
+    out, lse = E.attention(q.detach(), k.detach(), v.detach(), plan, scale=0.2, lse=True)
+    want = E.attention_backward(up.contiguous(), q.detach(), k.detach(), v.detach(), out, lse, plan, scale=0.2)
+    assert all(torch.equal(t.grad, g) for t, g in zip((q, k, v), want))
+
+
+def test_plans_made_again_give_the_same_bits():
+    # the order of equal items in a plan may vary from one to the next; what is cut and joined does not
+    E = _enc()
+    lq, lk, hq, hk, d = [1, 3, 1, 1, 200, 1] * 4, [4000, 4097, 700, 4000, 4000, 2500] * 4, 8, 2, 128
+    q, do = (_randn(s, sum(lq), hq, d, dtype=BF) for s in (134, 135))
+    k, v = (_randn(s, sum(lk), hk, d, dtype=BF) for s in (136, 137))
+    cq, ck = _cu(lq), _cu(lk)
+    plan = E.AttentionPlan(cq, ck, sum(lq), sum(lk), hq, hk, d, causal=True)
+    want = None
+    for _ in range(8):
+        plan.update(cq, ck)
+        out, lse = E.attention(q, k, v, plan, lse=True)
+        got = (out, lse) + E.attention_backward(do, q, k, v, out, lse, plan)
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def _normal(seed, *shape):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, dtype=BF, device="cuda").normal_(generator=g)
+
+
+def test_layer_norm_past_two_to_the_31_elements():
+    E = _enc()
+    rows, width, tail = 140000, 16384, 50
+    x = _normal(140, rows, width)
+    dy = torch.zeros_like(x)
+    dy[-tail:] = _normal(141, tail, width)
+    w = _randn(142, width)
+    y, mean, rstd = E.layer_norm(x, w, stats=True)
+    y1, m1, r1 = E.layer_norm(x[-tail:], w, stats=True)
+    assert torch.equal(y[-tail:], y1) and torch.equal(mean[-tail:], m1) and torch.equal(rstd[-tail:], r1)
+    dx, dw, db = E.layer_norm_backward(dy, x, mean, rstd, w)
+    assert torch.equal(dx[-tail:], E.layer_norm_backward(dy[-tail:], x[-tail:], m1, r1, w)[0])
+    assert not dx[:-tail].any()
+    _, rdw, rdb, xh, _ = R.layer_norm_backward(dy[-tail:], x[-tail:], m1, r1, w)
+    a = dy[-tail:].double().abs()
+    R.close(dw, rdw, 32 * E32 * (a * xh.abs()).sum(0), "dweight")
+    R.close(db, rdb, 32 * E32 * a.sum(0), "dbias")
+
+
+def test_mrope_past_two_to_the_31_elements():
+    E = _enc()
+    rows, tail, axes = (1 << 20) + 77, 40, E.section_axes((24, 20, 20))
+    q, k = _normal(143, rows, 16, 128), _normal(144, rows, 1, 128)
+    pos = torch.arange(3 * rows, dtype=torch.int32, device="cuda").view(3, rows) % 40000
+    oq, ok = E.mrope_apply(q, k, pos, axes)
+    tq, tk = E.mrope_apply(q[-tail:].contiguous(), k[-tail:].contiguous(), pos[:, -tail:].contiguous(), axes)
+    assert torch.equal(oq[-tail:], tq) and torch.equal(ok[-tail:], tk)
+
+
+def test_attention_over_caches_past_two_to_the_31_elements():
+    E = _enc()
+    lens, hq, hk, d = [1100000, 700000, 300000, 5000, 777], 16, 8, 128
+    rows = sum(lens)
+    k, v, q = _normal(145, rows, hk, d), _normal(146, rows, hk, d), _randn(147, len(lens), hq, d, dtype=BF)
+    plan = E.AttentionPlan(_cu([1] * len(lens)), _cu(lens), len(lens), rows, hq, hk, d, causal=True)
+    out, lse = E.attention(q, k, v, plan, lse=True)
+    at = rows
+    for i in reversed(range(len(lens))):
+        n, at = lens[i], at - lens[i]
+        if n > 400000:
+            continue
+        r = R.attention(q[i:i + 1], k[at:at + n], v[at:at + n], [1], [n], True)
+        err = T._score_error(r["score"], d)
+        R.close(lse[i:i + 1], r["lse"], err + 8 * E32 * (1 + r["lse"].abs()), "lse")
+        T._close_rounded(out[i:i + 1], r, "out", BF, 2 * err)
+
+
+def test_attention_gradients_past_two_to_the_31_elements():
+    E = _enc()
+    n, seqs, h, d = 128, 8300, 16, 128
+    rows = n * seqs + 60
+    lens = [n] * seqs + [60]
+    q, k, v, do = (_normal(148 + i, rows, h, d) for i in range(4))
+    plan = E.AttentionPlan(_cu(lens), _cu(lens), rows, rows, h, h, d, causal=True)
+    out, lse = E.attention(q, k, v, plan, lse=True)
+    got = E.attention_backward(do, q, k, v, out, lse, plan)
+    last = [t[-60:].contiguous() for t in (q, k, v, do)]
+    alone = E.AttentionPlan(_cu([60]), _cu([60]), 60, 60, h, h, d, causal=True)
+    o1, l1 = E.attention(*last[:3], alone, lse=True)
+    assert torch.equal(out[-60:], o1) and torch.equal(lse[-60:], l1)
+    for a, b in zip(got, E.attention_backward(last[3], *last[:3], o1, l1, alone)):
+        assert torch.equal(a[-60:], b)
