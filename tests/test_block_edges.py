@@ -97,6 +97,8 @@ def test_gradients_of_gradients_are_refused(monkeypatch):
 
 
 class _Stream:
+    cuda_stream = 5
+
     def __init__(self, device_index):
         self.device_index = device_index
 
@@ -118,7 +120,8 @@ def test_a_raw_stream_handle_is_one_of_the_tensors_gpu(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", _Stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", Made)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: 5)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: _Stream(1))
+    monkeypatch.setattr(E, "_raw_stream", lambda d: _Stream.cuda_stream)
     monkeypatch.setattr(E, "_launch", lambda name, device, *a: launched.append((name, device)))
     x, stat, pos = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4), torch.zeros(3, 4, dtype=torch.int32)
     q, cu = x.view(4, 2, 8), torch.tensor([0, 4], dtype=torch.int32)
@@ -160,7 +163,8 @@ def test_status_pairs_and_counts_of_the_wrong_size_or_type_are_refused(monkeypat
     launched = []
     monkeypatch.setattr(E, "_device", lambda *t: 1)
     monkeypatch.setattr(E, "_current", lambda stream, x: contextlib.nullcontext())
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: 5)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: _Stream(1))
+    monkeypatch.setattr(E, "_raw_stream", lambda d: _Stream.cuda_stream)
     monkeypatch.setattr(E, "_launch", lambda name, *a: launched.append(name))
     x = torch.zeros(4, 2, 8, dtype=torch.bfloat16)
     cu, lse, spans = torch.tensor([0, 4], dtype=torch.int32), torch.zeros(4, 2), torch.zeros(1, 4, dtype=torch.int32)
@@ -195,3 +199,23 @@ def test_the_module_imports_under_a_torch_without_cuda(monkeypatch):
     spec.loader.exec_module(again)
     with pytest.raises(ValueError):
         again.layer_norm(torch.zeros(2, 8))              # not on a GPU
+
+
+def test_a_plan_used_on_another_stream_is_recorded_there(monkeypatch):
+    recorded = []
+    now = _Stream(1)
+    monkeypatch.setattr(E, "_device", lambda *t: 1)
+    monkeypatch.setattr(E, "_current", lambda stream, x: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: now)
+    monkeypatch.setattr(E, "_raw_stream", lambda d: now.cuda_stream)
+    monkeypatch.setattr(E, "_launch", lambda *a: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t, s)))
+    x, cu = torch.zeros(4, 2, 8, dtype=torch.bfloat16), torch.tensor([0, 4], dtype=torch.int32)
+    plan = E.AttentionPlan(cu, cu, 4, 4, 2, 2, 8)
+    E.attention(x, x, x, plan)
+    E.attention_backward(x, x, x, x, x, torch.zeros(4, 2), plan)
+    assert not recorded                                  # its own stream
+    now.cuda_stream = 9
+    E.attention(x, x, x, plan)
+    E.attention_backward(x, x, x, x, x, torch.zeros(4, 2), plan)
+    assert [(t is plan.buffer, s is now) for t, s in recorded] == [(True, True)] * 2

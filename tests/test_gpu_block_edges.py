@@ -418,3 +418,35 @@ def test_attention_gradients_past_two_to_the_31_elements():
     assert torch.equal(out[-60:], o1) and torch.equal(lse[-60:], l1)
     for a, b in zip(got, E.attention_backward(last[3], *last[:3], o1, l1, alone)):
         assert torch.equal(a[-60:], b)
+
+
+# ------------------------------------------------------------------ streams
+
+def test_a_plan_dropped_before_its_call_has_run_on_another_stream():
+    # its memory is not handed out again before that call is done (what would be, is zeroed: an empty plan)
+    E = _enc()
+    rows, h, d = 700, 2, 64
+    cu = _cu([rows])
+    q, k, v = (_randn(150 + i, rows, h, d, dtype=BF) for i in range(3))
+    do = _randn(153, rows, h, d, dtype=BF)
+    keep = E.AttentionPlan(cu, cu, rows, rows, h, h, d)
+    want, lse = E.attention(q, k, v, keep, lse=True)
+    grads = E.attention_backward(do, q, k, v, want, lse, keep)
+    side, size = torch.cuda.Stream(), keep.buffer.numel()
+    for inside in (False, True):
+        plan = E.AttentionPlan(cu, cu, rows, rows, h, h, d)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)               # some 0.1 s: the call below starts behind it
+        if inside:
+            with torch.cuda.stream(side):
+                out = E.attention(q, k, v, plan)
+                got = E.attention_backward(do, q, k, v, want, lse, plan)
+        else:
+            out = E.attention(q, k, v, plan, stream=side)
+            got = E.attention_backward(do, q, k, v, want, lse, plan, stream=side)
+        del plan
+        taken = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(20)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and len(taken) == 20
+        assert all(torch.equal(a, b) for a, b in zip(got, grads))

@@ -288,6 +288,7 @@ class AttentionPlan:
         with _current(stream if stream is not None else torch.cuda.current_stream(cu_q.device), cu_q):
             size = B.vitfe_attention_plan_bytes(self.shape)
             self.buffer = torch.empty(max(size, 16), dtype=torch.uint8, device=cu_q.device)
+            self._home = torch.cuda.current_stream(cu_q.device).cuda_stream
             self.update(cu_q, cu_k, status)
 
     def update(self, cu_q, cu_k, status=None, stream=None) -> None:
@@ -307,6 +308,13 @@ class AttentionPlan:
         self.version += 1
         _launch("vitfe_attention_plan", device, self.shape, cu_q.data_ptr(), cu_k.data_ptr(), self.buffer.data_ptr(),
                 status)
+
+    def address(self, device: int) -> int:
+        """The buffer's address for a call on the current stream; a plan that goes away before that call
+        has run leaves its memory to it, whichever stream it was made on."""
+        if _raw_stream(device) != self._home:
+            self.buffer.record_stream(torch.cuda.current_stream(device))
+        return self.buffer.data_ptr()
 
     def of(self, q, k, v) -> "B.AttentionShape":
         """The shape of a call with these tensors; raises where they do not fit the plan."""
@@ -331,7 +339,7 @@ def attention(q, k, v, plan: AttentionPlan, scale: Optional[float] = None, lse: 
     out = _target(q, out, "out")
     sums = _empty(plan._q[:2], dtype=_float32, device=q.device) if lse else None
     work = _empty(plan._work, dtype=torch.uint8, device=q.device) if plan._work else None
-    _launch("vitfe_attention", device, shape, plan.buffer.data_ptr(), q.data_ptr(), _heads(q, "q"), k.data_ptr(),
+    _launch("vitfe_attention", device, shape, plan.address(device), q.data_ptr(), _heads(q, "q"), k.data_ptr(),
             _heads(k, "k"), v.data_ptr(), _heads(v, "v"), q.shape[2] ** -0.5 if scale is None else scale,
             out.data_ptr(), _heads(out, "out"), _ptr(sums), _ptr(work), _words(status, 2, "status"))
     return (out, sums) if lse else out
@@ -352,7 +360,7 @@ def attention_backward(dout, q, k, v, out, lse, plan: AttentionPlan, scale: Opti
         raise ValueError("lse: the forward pass's float32 [rows][heads] is needed")
     dq, dk, dv = _like(q), _like(k), _like(v)
     work = _empty(plan._work_backward, dtype=torch.uint8, device=q.device) if plan._work_backward else None
-    _launch("vitfe_attention_backward", device, shape, plan.buffer.data_ptr(), dout.data_ptr(), _heads(dout, "dout"),
+    _launch("vitfe_attention_backward", device, shape, plan.address(device), dout.data_ptr(), _heads(dout, "dout"),
             q.data_ptr(), _heads(q, "q"), k.data_ptr(), _heads(k, "k"), v.data_ptr(), _heads(v, "v"), out.data_ptr(),
             _heads(out, "out"), lse.data_ptr(), q.shape[2] ** -0.5 if scale is None else scale, dq.data_ptr(),
             _heads(dq, "dq"), dk.data_ptr(), _heads(dk, "dk"), dv.data_ptr(), _heads(dv, "dv"), _ptr(work),
