@@ -306,9 +306,10 @@ __host__ __device__ constexpr int backward_per_sm(int C) { return C <= 8 ? 3 : C
 // Backward: rows of x and dout arrive in shared memory through a ring of bulk copies that the
 // group's first thread keeps `stages` rows ahead (registers hold the parameter sums, not rows in
 // flight), and are read twice: for the sums, then for
-//   dx = dout (rstd w) + (x - mean) A + B,  A = -rstd^2 mean(g xh),  B = -rstd mean(g).
+//   dx = rstd (dout w + (x - mean) A + B),  A = -rstd mean(g xh),  B = -mean(g).
 // The mean is subtracted first, as in the forward pass: x rstd - mean rstd would lose the digits that
-// rows far from zero have in common.
+// rows far from zero have in common.  (It costs an addition a pair: 589,824 x 1280 684 -> 687 us, rows of
+// 1027, which move single elements, 167 -> 173; rstd inside A and B, a register pair more, 691 and 186.)
 // Each block leaves one row of parameter sums, in a fixed order: no atomics, the same bits every time.
 // bf16, 589,824 x 1280: 685 us, 6.6 TB/s, 98% of what a copy reaches.  18,048 x 1280: 37 us where the
 // bytes need 20: the start, the blocks' sums and the kernel that adds them are some 17 us of it,
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
     }
     float s[2] = {lo_f32(s1) + hi_f32(s1), lo_f32(s2) + hi_f32(s2)};
     group_sum<T>(s, red, g, turn);
-    const float fa = -rstd * rstd * (s[1] * rstd * inv_n), fb = -rstd * (s[0] * inv_n);
+    const float fa = -rstd * rstd * (s[1] * inv_n), fb = -(s[0] * inv_n);
     const uint64_t pa = f32x2(fa, fa), pb = f32x2(fb, fb);
     X* dx = static_cast<X*>(a.out) + r * a.out_stride + t * V;
 #pragma unroll
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kNormThreads, backward_per_sm(C)) norm_backwar
       load_params<V, T, C>(smem_u32(weight), i, t, w);
 #pragma unroll
       for (int p = 0; p < P; ++p)
-        fx[p] = fma_f32x2(fd[p], mul_f32x2(w[p], rs), fma_f32x2(add_f32x2(fx[p], minus), pa, pb));
+        fx[p] = mul_f32x2(fma_f32x2(fd[p], w[p], fma_f32x2(add_f32x2(fx[p], minus), pa, pb)), rs);
       store_chunk<X, V, T, C>(dx, i, t, width, fx);
     }
     group_sync<T>(g);                         // the slot has been read
