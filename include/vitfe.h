@@ -355,7 +355,9 @@ vitfe_status vitfe_mrope_apply(const int32_t* pos, int32_t axes, const uint8_t* 
                                int64_t k_out_row_stride, cudaStream_t stream);
 
 /* Attention over packed sequences.  Sequence s holds the query rows
- * [cu_q[s], cu_q[s+1]) and the key rows [cu_k[s], cu_k[s+1]); either may be empty.
+ * [cu_q[s], cu_q[s+1]) and the key rows [cu_k[s], cu_k[s+1]); either may be empty
+ * (sequences follow each other without gaps: a cache with room behind each, or in
+ * pages, is not a form of this call).
  * Query head h reads key head h / (heads_q / heads_kv).
  *   out = softmax(scale * q k^T) v over the keys that the row sees.
  * causal: the last query row of a sequence sees all its keys, the one before it
@@ -377,7 +379,8 @@ typedef struct {
 /* The plan of a batch: which tiles of which sequences there are, largest first, and
  * how long key ranges are cut for few query rows.  Made on the device from the
  * boundaries (so a captured graph replays with new ones), once for all layers of a
- * batch; read-only afterwards, so calls on several streams may share it.
+ * batch; read-only afterwards, so calls on several streams may share it; gradients
+ * need the plan of their forward pass.
  * cu_q, cu_k (device int32 [max_seqs + 1]; the layout of vitfe_cu_seqlens, whose
  * entries past the last sequence repeat its end).  Boundaries that decrease, do not
  * start at 0 or pass rows_q / rows_k: status {VITFE_EDEVICE_DESC, sequence}, and the

@@ -5,7 +5,7 @@
 Two stills and a short video go through the front end (embeddings, RoPE tables, sequence
 boundaries) and one encoder block, forward and backward.  Then a prompt of text and those items
 gets its three-axis positions, and its queries and keys are rotated and attended, causally, first
-as a whole and then one token at a time: the last row has to come out the same both ways.
+as a whole and then its last token alone: that row has to come out the same both ways.
 """
 from __future__ import annotations
 

@@ -311,7 +311,7 @@ __host__ __device__ constexpr int backward_per_sm(int C) { return C <= 8 ? 3 : C
 // rows far from zero have in common.  (It costs an addition a pair: 589,824 x 1280 684 -> 687 us, rows of
 // 1027, which move single elements, 167 -> 173; rstd inside A and B, a register pair more, 691 and 186.)
 // Each block leaves one row of parameter sums, in a fixed order: no atomics, the same bits every time.
-// bf16, 589,824 x 1280: 685 us, 6.6 TB/s, 98% of what a copy reaches.  18,048 x 1280: 37 us where the
+// bf16, 589,824 x 1280: 687 us, 6.6 TB/s, 97% of what a copy reaches.  18,048 x 1280: 38 us where the
 // bytes need 20: the start, the blocks' sums and the kernel that adds them are some 17 us of it,
 // whatever the rows (9 us where only dx is asked for).
 template <typename X, int V, int T, int C>
